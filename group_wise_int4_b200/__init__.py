@@ -9,6 +9,7 @@ are not given are allocated with torch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -74,6 +75,16 @@ class flex_kv_cache(ctypes.Structure):
                 ("max_seq", ctypes.c_int32), ("cfg", flexq_config), ("valid_from", ctypes.c_void_p)]
 
 
+class flex_paged_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_meta", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("cfg", flexq_config)]
+
+
 _I32, _I64, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _SIGS = {
     "flexq_codes_bytes": (_I64, [_I32, ctypes.POINTER(ctypes.c_int64), flexq_config]),
@@ -102,6 +113,13 @@ _SIGS = {
     "flex_embed": (_I32, [ctypes.POINTER(flexq_tensor), _I32, _P, _I32, _P, _P, _I64, _P, _P]),
     "flex_lm_head_ws_bytes": (_I64, [ctypes.POINTER(flexq_tensor), _I32, _I64, _I32]),
     "flex_lm_head_argmax": (_I32, [ctypes.POINTER(flexq_tensor), _I32, _P, _P, _P, _I64, _P, _P, _P, _I64, _P]),
+    "flex_paged_store_kv": (_I32, [ctypes.POINTER(flex_paged_cache), _P, _P, _I64, _P, _I32, _I32, _I32, _P, _P]),
+    "flex_paged_load_kv": (_I32, [ctypes.POINTER(flex_paged_cache), _P, _P, _I64, _P, _I32, _I32, _I32, _P, _P]),
+    "flex_paged_attention_ws_bytes": (_I64, [ctypes.POINTER(flex_paged_cache), _I32, _I32, _I32, _I32, _I32]),
+    "flex_paged_attention": (_I32, [ctypes.POINTER(flex_paged_cache), _P, _I64, _I32, _P, _P, _I64, _P, _P, _P,
+                                    _I32, _I32, _I32, _I32, _P, _I64, _P]),
+    "flex_paged_evict_ws_bytes": (_I64, [ctypes.POINTER(flex_paged_cache), _I32]),
+    "flex_paged_evict": (_I32, [ctypes.POINTER(flex_paged_cache), _I32, _I32, _P, _P, _I64, _P]),
     "flex_get_status": (_I32, [_P]),
     "flex_set_wait_limit_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
     "flex_set_gemm_gate": (_P, [_P]),
@@ -112,7 +130,7 @@ _SIGS = {
     "flex_abi_layout": (_I64, [_I32, _I32]),
 }
 
-_STRUCTS = (flexq_config, flexq_tensor, flex_layer, flex_kv_cache)   # flex_abi_layout's `which` order
+_STRUCTS = (flexq_config, flexq_tensor, flex_layer, flex_kv_cache, flex_paged_cache)   # flex_abi_layout's `which` order
 
 
 def _check_layout(L):
@@ -456,6 +474,224 @@ def flex_lm_head_argmax(E: "CompressedWeight", vocab, lnf_g, lnf_b, x, ws, next_
                                    ctypes.c_void_p(_stream(stream)))
     _check(rc, "flex_lm_head_argmax")
     return next_ids
+
+
+# ---- paged compressed KV cache --------------------------------------------------------
+class FlexPagedCache:
+    """Paged compressed KV cache of one layer (flex_paged_cache).
+
+    page_table: int32 CUDA tensor [batch][max_pages]; ctx_len: int32 CUDA tensor [batch], the
+    slots each sequence holds. Both are read by the kernels when they run and may be
+    shared by the caches of several layers.
+    The pools are allocated (zeroed) for num_pages pages, or taken from `pools`, a tuple
+    (k_codes, k_meta, v_codes, v_meta): codes uint8 [num_pages][n_kv_heads][page_size]
+    [head_dim*bits/8], meta fp16 [num_pages][n_kv_heads][page_size][head_dim/group][2].
+    weight: True, or an fp32 tensor [num_pages][n_kv_heads][page_size], to accumulate
+    attention weights; slot_pos: the same with int32, to keep positions. Eviction needs
+    both."""
+
+    def __init__(self, page_table, ctx_len, num_pages=None, page_size=None, n_kv_heads=None, head_dim=None,
+                 num_bits=4, group_size=64, pools=None, weight=None, slot_pos=None):
+        dev = self.device = page_table.device
+        self.cfg = config(num_bits, group_size, 3)
+        if pools is None:
+            shape = (int(num_pages), int(n_kv_heads), int(page_size))
+            code = dict(dtype=torch.uint8, device=dev)
+            meta = dict(dtype=torch.float16, device=dev)
+            kb, ng = head_dim * num_bits // 8, head_dim // group_size
+            pools = (torch.zeros(shape + (kb,), **code), torch.zeros(shape + (ng, 2), **meta),
+                     torch.zeros(shape + (kb,), **code), torch.zeros(shape + (ng, 2), **meta))
+        self.k_codes, self.k_meta, self.v_codes, self.v_meta = pools
+        shape = tuple(self.k_codes.shape[:3])
+        self.num_pages, self.n_kv_heads, self.page_size = shape
+        self.head_dim = self.k_codes.shape[-1] * 8 // num_bits
+        if weight is True:
+            weight = torch.zeros(shape, dtype=torch.float32, device=dev)
+        if slot_pos is True:
+            slot_pos = torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.page_table, self.ctx_len, self.weight, self.slot_pos = page_table, ctx_len, weight, slot_pos
+        self.batch, self.max_pages = page_table.shape
+        self.struct()
+
+    def __setattr__(self, name, value):
+        # another tensor in a place the C struct points at: the struct is made (and checked) again
+        super().__setattr__(name, value)
+        if name != "_struct" and name != "_ref":
+            super().__setattr__("_struct", None)
+
+    def struct(self) -> flex_paged_cache:
+        if self._struct is None:
+            dev, bits, group = self.device, self.cfg.num_bits, self.cfg.group_size
+            shape = (self.num_pages, self.n_kv_heads, self.page_size)
+            _need(self.page_table, torch.int32, dev, "page_table", (self.batch, self.max_pages))
+            _need(self.ctx_len, torch.int32, dev, "ctx_len", (self.batch,))
+            for name in ("k", "v"):
+                _need(getattr(self, name + "_codes"), torch.uint8, dev, name + "_codes",
+                      shape + (self.head_dim * bits // 8,))
+                _need(getattr(self, name + "_meta"), torch.float16, dev, name + "_meta",
+                      shape + (self.head_dim // group, 2))
+            if self.weight is not None:
+                _need(self.weight, torch.float32, dev, "weight", shape)
+            if self.slot_pos is not None:
+                _need(self.slot_pos, torch.int32, dev, "slot_pos", shape)
+            s = flex_paged_cache()
+            for name in ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "slot_pos", "page_table", "ctx_len"):
+                t = getattr(self, name)
+                setattr(s, name, None if t is None else t.data_ptr())
+            for name in ("num_pages", "page_size", "max_pages", "batch", "n_kv_heads", "head_dim", "cfg"):
+                setattr(s, name, getattr(self, name))
+            self._struct, self._ref = s, ctypes.byref(s)
+        return self._struct
+
+    def ref(self):
+        self.struct()
+        return self._ref
+
+
+def _need(t, dtype, device, name, shape=None):
+    """A contiguous tensor of this dtype, device and shape (None: any extent)."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+    if not t.is_contiguous() or (shape is not None and (t.dim() != len(shape) or any(
+            d is not None and d != e for d, e in zip(shape, t.shape)))):
+        raise ValueError(f"{name}: a contiguous tensor of shape {shape} expected, got {tuple(t.shape)}")
+
+
+def _need_rows(t, dtype, device, name, total, stride, width):
+    """Rows of `stride` elements, the first `width` of which are used, lie within the tensor's memory."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if total and (stride < width or (total - 1) * stride + width > have):
+        raise ValueError(f"{name}: {total} rows of {stride} elements expected, {have} elements are there")
+
+
+def _rows_call(cache, cu, most, total, batch):
+    """(batch, total) of a ragged call, checked against cu's length."""
+    if cu is None:
+        batch = cache.batch if batch is None else int(batch)
+        total = batch * int(most)
+    else:
+        _need(cu, torch.int32, cache.device, "cu", (None,))
+        batch = cu.shape[0] - 1 if batch is None else int(batch)
+        if cu.shape[0] < batch + 1:
+            raise ValueError(f"cu: {batch + 1} offsets expected, got {cu.shape[0]}")
+        if total is None:
+            raise ValueError("total: the number of rows that cu may reach is needed with cu")
+    return batch, int(total)
+
+
+def _vec(t, cache, batch, name):
+    """Address of an optional int32 [batch] tensor."""
+    if t is None:
+        return None
+    _need(t, torch.int32, cache.device, name, (None,))
+    if t.shape[0] < batch:
+        raise ValueError(f"{name}: {batch} entries expected, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+def _on(cache, stream):
+    """Device of the cache made current, and the stream there."""
+    dev = cache.device.index
+    if dev is None:
+        raise ValueError(f"cache: a CUDA device expected, got {cache.device}")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream(stream)
+    return (_NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)), stream
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def flex_paged_store_kv(cache: FlexPagedCache, k_new, v_new, row_stride, cu_new, most, pos0=None, total=None,
+                        batch=None, stream=None):
+    """Quantise new rows into the slots behind ctx_len. cu_new: int32 [batch + 1] row offsets (then
+    `total` rows are there) or None (`most` rows each)."""
+    batch, total = _rows_call(cache, cu_new, most, total, batch)
+    width = cache.n_kv_heads * cache.head_dim
+    _need_rows(k_new, torch.float16, cache.device, "k_new", total, row_stride, width)
+    _need_rows(v_new, torch.float16, cache.device, "v_new", total, row_stride, width)
+    pos0 = _vec(pos0, cache, batch, "pos0")
+    guard, st = _on(cache, stream)
+    with guard:
+        rc = lib().flex_paged_store_kv(cache.ref(), k_new.data_ptr(), v_new.data_ptr(), row_stride,
+                                       None if cu_new is None else cu_new.data_ptr(), batch, total, most,
+                                       pos0, st)
+    _check(rc, "flex_paged_store_kv")
+
+
+def flex_paged_load_kv(cache: FlexPagedCache, k_out, v_out, row_stride, cu_rows, most, start=None, total=None,
+                       batch=None, stream=None):
+    """Dequantise slots start[b] + i (start None: 0) into rows cu_rows[b] + i."""
+    batch, total = _rows_call(cache, cu_rows, most, total, batch)
+    width = cache.n_kv_heads * cache.head_dim
+    _need_rows(k_out, torch.float16, cache.device, "k_out", total, row_stride, width)
+    _need_rows(v_out, torch.float16, cache.device, "v_out", total, row_stride, width)
+    start = _vec(start, cache, batch, "start")
+    guard, st = _on(cache, stream)
+    with guard:
+        rc = lib().flex_paged_load_kv(cache.ref(), k_out.data_ptr(), v_out.data_ptr(), row_stride,
+                                      None if cu_rows is None else cu_rows.data_ptr(), batch, total, most,
+                                      start, st)
+    _check(rc, "flex_paged_load_kv")
+
+
+def _size(n, what):
+    """A size query's result: bytes, or the error it stands for."""
+    if n < 0:
+        raise FlexError(int(n), what)
+    return int(n)
+
+
+def flex_paged_attention_ws_bytes(cache: FlexPagedCache, n_heads, total, most, accumulate=False, batch=None) -> int:
+    guard, _ = _on(cache, 0)
+    with guard:
+        n = lib().flex_paged_attention_ws_bytes(cache.ref(), n_heads, cache.batch if batch is None else batch, total,
+                                                most, 1 if accumulate else 0)
+    return _size(n, "flex_paged_attention_ws_bytes")
+
+
+def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_new, kv_stride, o, lse, cu_new, most, ws,
+                         accumulate=False, total=None, batch=None, stream=None):
+    """Attention of new tokens over the cached slots and their own fresh keys/values (k_new and
+    v_new None: cross attention, over the slots alone). lse: fp32 [total][n_heads] or None."""
+    batch, total = _rows_call(cache, cu_new, most, total, batch)
+    dev, dim = cache.device, cache.head_dim
+    _need_rows(q, torch.float16, dev, "q", total, q_stride, n_heads * dim)
+    _need_rows(o, torch.float16, dev, "o", total, n_heads * dim, n_heads * dim)
+    if k_new is not None:
+        _need_rows(k_new, torch.float16, dev, "k_new", total, kv_stride, cache.n_kv_heads * dim)
+    if v_new is not None:
+        _need_rows(v_new, torch.float16, dev, "v_new", total, kv_stride, cache.n_kv_heads * dim)
+    if lse is not None:
+        _need_rows(lse, torch.float32, dev, "lse", total, n_heads, n_heads)
+    guard, st = _on(cache, stream)
+    with guard:
+        rc = lib().flex_paged_attention(cache.ref(), q.data_ptr(), q_stride, n_heads,
+                                        None if k_new is None else k_new.data_ptr(),
+                                        None if v_new is None else v_new.data_ptr(), kv_stride, o.data_ptr(),
+                                        None if lse is None else lse.data_ptr(),
+                                        None if cu_new is None else cu_new.data_ptr(), batch, total, most,
+                                        1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    _check(rc, "flex_paged_attention")
+
+
+def flex_paged_evict_ws_bytes(cache: FlexPagedCache, budget) -> int:
+    return _size(lib().flex_paged_evict_ws_bytes(cache.ref(), budget), "flex_paged_evict_ws_bytes")
+
+
+def flex_paged_evict(cache: FlexPagedCache, budget, recent, new_len, ws, stream=None):
+    """Keep `budget` slots of every longer sequence and key head: the `recent` latest positions, then
+    the largest weights. new_len (int32 [batch]) takes min(ctx_len, budget)."""
+    _need(new_len, torch.int32, cache.device, "new_len", (cache.batch,))
+    guard, st = _on(cache, stream)
+    with guard:
+        rc = lib().flex_paged_evict(cache.ref(), budget, recent, new_len.data_ptr(), ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), st)
+    _check(rc, "flex_paged_evict")
 
 
 def flex_abi_layout(which: int, field: int) -> int:

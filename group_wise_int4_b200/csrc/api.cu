@@ -126,6 +126,15 @@ extern "C" int64_t flex_abi_layout(int32_t which, int32_t field) {
                         offsetof(flex_kv_cache, batch), offsetof(flex_kv_cache, n_heads),
                         offsetof(flex_kv_cache, head_dim), offsetof(flex_kv_cache, max_seq),
                         offsetof(flex_kv_cache, cfg), offsetof(flex_kv_cache, valid_from))
+        case 4:
+            FLEX_FIELDS(flex_paged_cache, offsetof(flex_paged_cache, k_codes), offsetof(flex_paged_cache, k_meta),
+                        offsetof(flex_paged_cache, v_codes), offsetof(flex_paged_cache, v_meta),
+                        offsetof(flex_paged_cache, weight), offsetof(flex_paged_cache, slot_pos),
+                        offsetof(flex_paged_cache, page_table), offsetof(flex_paged_cache, ctx_len),
+                        offsetof(flex_paged_cache, num_pages), offsetof(flex_paged_cache, page_size),
+                        offsetof(flex_paged_cache, max_pages), offsetof(flex_paged_cache, batch),
+                        offsetof(flex_paged_cache, n_kv_heads), offsetof(flex_paged_cache, head_dim),
+                        offsetof(flex_paged_cache, cfg))
         default:
             return -1;
     }

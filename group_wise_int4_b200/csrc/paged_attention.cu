@@ -1,0 +1,924 @@
+// Attention of new tokens over a paged compressed KV cache.
+//
+// For row r (token i of sequence b, query head h, key head g = h / share):
+//   s_j = q_r . k_j over the slots j < ctx_len[b] and the fresh tokens 0..i,
+//   lse_r = log sum_j exp(s_j),  o_r = sum_j exp(s_j - lse_r) v_j,
+// in one pass over the keys with a running maximum and sum; statistics are fp32 and in
+// base 2 (scores times log2 e), probabilities are rounded to fp16 once, as operands of the
+// value product: at most 2^-11 of each, far below o's own fp16 rounding after the sum.
+// k_j and v_j are the fp16 values of paged.cuh, so the products are exact and summed in fp32.
+#include <float.h>
+
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace flexq {
+namespace {
+
+__device__ __forceinline__ void cp16(uint32_t s, const void* g, bool ok) {
+    const int n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t s, const void* g, bool ok) {
+    const int n = ok ? N : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(s), "l"(g), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands
+__device__ __forceinline__ void mma168(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mat_trans(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// ---- operands -------------------------------------------------------------------------
+//
+// Scores are S^T = K Q^T: keys are the rows of the 16 x 8 products, query rows the columns.
+// Lane (g, t) of a quad row takes the dims [t D/4, (t+1) D/4) of its keys, so a key's codes
+// are one contiguous piece per lane; the product does not care which dims a k-step holds
+// as long as both operands agree. At 4 bits the nibble pairs of a word are (d, d+4),
+// (d+1, d+5), ..., at 8 bits the byte pairs are neighbours; the query is laid out to match.
+
+// Query operand of row g of an 8-row tile: D/16 k-steps of two registers.
+template <int D, int BITS>
+__device__ __forceinline__ void load_query(uint32_t (&bq)[D / 16][2], const __half* row, int t, bool ok) {
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {                 // 8 dims: two k-steps
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (ok) x = __ldg(reinterpret_cast<const uint4*>(row + t * (D / 4)) + u);
+        if (BITS == 4) {
+            bq[2 * u][0] = byte_perm(x.x, x.z, 0x5410u);
+            bq[2 * u][1] = byte_perm(x.x, x.z, 0x7632u);
+            bq[2 * u + 1][0] = byte_perm(x.y, x.w, 0x5410u);
+            bq[2 * u + 1][1] = byte_perm(x.y, x.w, 0x7632u);
+        } else {
+            bq[2 * u][0] = x.x;
+            bq[2 * u][1] = x.y;
+            bq[2 * u + 1][0] = x.z;
+            bq[2 * u + 1][1] = x.w;
+        }
+    }
+}
+
+// Key operand of two k-steps (8 dims) from 8 codes: at 4 bits one word, at 8 bits two.
+template <int BITS>
+__device__ __forceinline__ void key_pairs(uint32_t (&a)[4], uint32_t w0, uint32_t w1, uint32_t step, uint32_t mn) {
+    if (BITS == 4) {
+        const uint32_t y = w0 >> 8;
+        a[0] = h2_fma(codes_lo(w0), step, mn);
+        a[1] = h2_fma(codes_hi(w0), step, mn);
+        a[2] = h2_fma(codes_lo(y), step, mn);
+        a[3] = h2_fma(codes_hi(y), step, mn);
+    } else {
+        a[0] = h2_fma(codes_b01(w0), step, mn);
+        a[1] = h2_fma(codes_b23(w0), step, mn);
+        a[2] = h2_fma(codes_b01(w1), step, mn);
+        a[3] = h2_fma(codes_b23(w1), step, mn);
+    }
+}
+// The same from 8 fresh fp16 values.
+template <int BITS>
+__device__ __forceinline__ void key_pairs_fresh(uint32_t (&a)[4], uint4 x) {
+    if (BITS == 4) {
+        a[0] = byte_perm(x.x, x.z, 0x5410u);
+        a[1] = byte_perm(x.x, x.z, 0x7632u);
+        a[2] = byte_perm(x.y, x.w, 0x5410u);
+        a[3] = byte_perm(x.y, x.w, 0x7632u);
+    } else {
+        a[0] = x.x;
+        a[1] = x.y;
+        a[2] = x.z;
+        a[3] = x.w;
+    }
+}
+
+// Pairs of fp16 values: does one have the largest exponent (infinity or NaN), and the same
+// with those taken for 0.
+__device__ __forceinline__ uint32_t wild_halves(uint32_t x) { return __vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
+__device__ __forceinline__ bool any_wild(uint4 x) {
+    return (wild_halves(x.x) | wild_halves(x.y) | wild_halves(x.z) | wild_halves(x.w)) != 0u;
+}
+__device__ __forceinline__ uint4 without_wild(uint4 x) {
+    return make_uint4(x.x & ~wild_halves(x.x), x.y & ~wild_halves(x.y), x.z & ~wild_halves(x.z), x.w & ~wild_halves(x.w));
+}
+
+// ---- work split -------------------------------------------------------------------------
+//
+// A unit is (sequence, tile of R query rows, part of the key length); one block per unit
+// and key head. The key length of all sequences together is cut into parts of `part`
+// blocks of KEYS keys, so that about `target` blocks share it whatever its distribution:
+// every warp finds its block's unit by itself from ctx_len and cu (a few loads and
+// shuffles), so nothing has to be planned on the host or in another launch.
+struct RowsPlan {
+    int batch, share, target, heads;
+};
+
+struct Unit {
+    int b, tile, part, parts, per;      // per: key blocks in a part
+    int first, n, ctx;
+    bool live;
+};
+
+template <int R, int KEYS>
+__device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
+    const int lane = threadIdx.x & 31;
+    // work of the whole batch, in key blocks times row tiles
+    int64_t work = 0;
+    for (int b = lane; b < p.batch; b += 32) {
+        int first;
+        const int n = rows_of(rows, b, first, c.status);
+        const int64_t tiles = (static_cast<int64_t>(n) * p.share + R - 1) / R;
+        work += tiles * ((slots_of(c, b) + KEYS - 1) / KEYS);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    // at least two blocks of keys a part: less costs more to join than it saves
+    const int64_t even = (work * p.heads + p.target - 1) / p.target;
+    Unit u{};
+    u.per = static_cast<int>(even < 2 ? 2 : even > (1 << 30) ? (1 << 30) : even);
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int n = 0, ctx = 0, first = 0, tiles = 0, parts = 0;
+        if (b < p.batch) {
+            n = rows_of(rows, b, first, c.status);
+            ctx = slots_of(c, b);
+            tiles = static_cast<int>((static_cast<int64_t>(n) * p.share + R - 1) / R);
+            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.per - 1) / u.per);
+        }
+        const int64_t mine = static_cast<int64_t>(tiles) * parts;
+        int64_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        x += before;                                    // units up to and with b
+        const unsigned has = __ballot_sync(0xffffffffu, unit < x);
+        if (has) {
+            const int l = __ffs(has) - 1;
+            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, x - mine, l));
+            u.b = b0 + l;
+            u.n = __shfl_sync(0xffffffffu, n, l);
+            u.ctx = __shfl_sync(0xffffffffu, ctx, l);
+            u.first = __shfl_sync(0xffffffffu, first, l);
+            u.parts = __shfl_sync(0xffffffffu, parts, l);
+            u.tile = at / u.parts;
+            u.part = at % u.parts;
+            u.live = true;
+            return u;
+        }
+        before = __shfl_sync(0xffffffffu, x, 31);
+    }
+    return u;
+}
+
+// Where a row tile's parts are: written by its part 0 for the joining kernel.
+struct TileRecord {
+    int parts, slot;      // parts lie at partial slots [slot, slot + parts)
+};
+
+// ---- few rows: one warp's 16 keys against 8 or 16 query rows ------------------------------
+//
+// mma.sync m16n8k16 with the keys as its 16 rows: a decode step has 1 to 16 query rows per
+// key head, and a 128-row tcgen05 tile would be all padding. Each of 4 warps streams its
+// own keys through its part of a cp.async ring, dequantises in registers and keeps its own
+// maximum, sum and output (a transposed 16 x 8 tile per 16 dims); the warps are joined
+// once at the end. The value product O^T = V^T P^T needs P^T as its 8-column operand,
+// which movmatrix makes of the score tile; V^T comes from byte permutations of four keys'
+// codes, two keys to a register.
+template <int D, int BITS>
+struct RowsShape {
+    static constexpr int KB = D * BITS / 8;                // bytes of a key's codes
+    static constexpr int KW = KB >= 128 ? 16 : 32;         // keys of a warp and stage
+    static constexpr int KEYS = 4 * KW;
+    static constexpr int STAGES = 3;
+};
+
+// 16-byte piece i of a warp's KW keys, in keys' order, is put where the value product reads
+// without bank conflicts: lanes (g, t) read piece(s) g of keys 2t, 2t + 1, ....
+template <int KB>
+__device__ __forceinline__ int value_piece(int key, int c) {
+    if (KB == 128) return key * 8 + (c ^ (((key >> 1) & 3) << 1));
+    if (KB == 64) return (key ^ ((key >> 1) & 1)) * 4 + (c ^ (((key >> 2) & 1) << 1));
+    return (key ^ ((key >> 2) & 1)) * 2 + c;
+}
+
+template <int D, int BITS, int GS, int NR>
+__global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf rows, RowsPlan plan,
+                                                         const __half* __restrict__ q, int64_t q_stride,
+                                                         const __half* __restrict__ k_new,
+                                                         const __half* __restrict__ v_new, int64_t kv_stride,
+                                                         __half* __restrict__ o, float* __restrict__ lse,
+                                                         float* __restrict__ parts_ws, TileRecord* __restrict__ records,
+                                                         int most_tiles) {
+    using S = RowsShape<D, BITS>;
+    constexpr int KB = S::KB, KW = S::KW, KEYS = S::KEYS, ST = S::STAGES;
+    constexpr int NG = D / GS, R = 8 * NR, KT = KW / 16;
+    constexpr int CODE = KW * KB, META = KW * NG * 4, STAGE = 2 * CODE + 2 * META;      // bytes of a warp
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int head = blockIdx.x % plan.heads, unit = blockIdx.x / plan.heads;
+    const Unit u = find_unit<R, KEYS>(c, rows, plan, unit);
+    if (!u.live) return;
+    const int blocks = (u.ctx + KEYS - 1) / KEYS;
+    const int key0 = min(blocks, u.part * u.per) * KEYS;
+    const int key1 = min(u.ctx, min(blocks, (u.part + 1) * u.per) * KEYS);
+    const int stages = (key1 - key0 + KEYS - 1) / KEYS;
+    const int row_end = u.n * plan.share;                // rows of this sequence and key head
+    const int row0 = u.tile * R;
+
+    const uint32_t my_ring = smem_addr(ring) + warp * ST * STAGE;
+    // lane i of a stage looks up the row of its warp's key i (KW = 16: both halves alike)
+    auto row_index = [&](int s) {
+        const int j = key0 + s * KEYS + warp * KW + (lane & (KW - 1));
+        if (j >= key1) return -1;
+        const int p = page_of(c, u.b, j);
+        return p < 0 ? -1 : slot_row(c, p, head, j);
+    };
+    auto load_stage = [&](int s, int row) {
+        const uint32_t at = my_ring + (s % ST) * STAGE;
+#pragma unroll
+        for (int i = 0; i < CODE / 16 / 32; ++i) {
+            const int piece = lane + i * 32, key = piece / (KB / 16), part = piece % (KB / 16);
+            const int r = __shfl_sync(0xffffffffu, row, key);
+            const int64_t off = r < 0 ? 0 : static_cast<int64_t>(r) * KB + part * 16;
+            cp16(at + piece * 16, c.kc + off, r >= 0);
+            cp16(at + CODE + value_piece<KB>(key, part) * 16, c.vc + off, r >= 0);
+        }
+        if (lane < KW) {                                  // absent keys: min and scale 0, so the values are 0
+            const int64_t off = row < 0 ? 0 : static_cast<int64_t>(row) * NG;
+            cp_small<NG * 4>(at + 2 * CODE + lane * NG * 4, c.km + off, row >= 0);
+            cp_small<NG * 4>(at + 2 * CODE + META + lane * NG * 4, c.vm + off, row >= 0);
+        }
+    };
+    int row_next = stages > 0 ? row_index(0) : -1;
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) {
+        if (s < stages) {
+            const int r = row_next;
+            row_next = s + 1 < stages ? row_index(s + 1) : -1;
+            load_stage(s, r);
+        }
+        cp_commit();
+    }
+
+    // queries; the tokens of this lane's score columns (rows 2t, 2t + 1 of each tile)
+    uint32_t bq[NR][D / 16][2];
+    int token[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int r = row0 + n * 8 + g;
+        const bool ok = r < row_end;
+        const int i = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
+        load_query<D, BITS>(bq[n], q + static_cast<int64_t>(u.first + i) * q_stride + h * D, t, ok);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) token[n][e] = (row0 + n * 8 + 2 * t + e) / plan.share;
+    }
+
+    float m[NR][2], l[NR][2], acc[D / 16][NR][4];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        m[n][0] = m[n][1] = -FLT_MAX;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+    }
+
+    // Scores of T tiles of 16 keys (base 2, -inf where hidden) -> running maximum, sum,
+    // and the probabilities as the value product's operand.
+    auto softmax = [&](auto& sc, auto& pb, auto tiles_c) {
+        constexpr int T = decltype(tiles_c)::value;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float top[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
+#pragma unroll
+                for (int k = 1; k < T; ++k) top[e] = fmaxf(top[e], fmaxf(sc[k][n][e], sc[k][n][2 + e]));
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], w));
+                    top[e] = fmaxf(top[e], m[n][e]);
+                    const float f = exp2_fast(m[n][e] - top[e]);
+                    m[n][e] = top[e];
+                    l[n][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        acc[i][n][e] *= f;
+                        acc[i][n][2 + e] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(sc[k][n][e] - m[n][e & 1]);
+                l[n][0] += p[0] + p[2];
+                l[n][1] += p[1] + p[3];
+                pb[k][n][0] = mat_trans(half2_of(p[0], p[1]));
+                pb[k][n][1] = mat_trans(half2_of(p[2], p[3]));
+            }
+        }
+    };
+
+    // ---- fresh keys, by the last part: tile after tile of 16, shared out to the warps
+    if (k_new != nullptr && u.part == u.parts - 1) {
+        const int last = min(u.n, (min(row_end, row0 + R) - 1) / plan.share + 1);       // keys any row sees
+        const __half* kf = k_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
+        const __half* vf = v_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
+        for (int j0 = warp * 16; j0 < last; j0 += 64) {
+            float sc[1][NR][4];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) sc[0][n][0] = sc[0][n][1] = sc[0][n][2] = sc[0][n][3] = 0.f;
+            const bool ok0 = j0 + g < last, ok8 = j0 + g + 8 < last;
+            const uint4* x0 = reinterpret_cast<const uint4*>(kf + static_cast<int64_t>(ok0 ? j0 + g : 0) * kv_stride + t * (D / 4));
+            const uint4* x8 = reinterpret_cast<const uint4*>(kf + static_cast<int64_t>(ok8 ? j0 + g + 8 : 0) * kv_stride + t * (D / 4));
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t a[4], z[4];
+                key_pairs_fresh<BITS>(a, ok0 ? __ldg(x0 + w) : make_uint4(0, 0, 0, 0));
+                key_pairs_fresh<BITS>(z, ok8 ? __ldg(x8 + w) : make_uint4(0, 0, 0, 0));
+                const uint32_t a0[4] = {a[0], z[0], a[1], z[1]}, a1[4] = {a[2], z[2], a[3], z[3]};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    mma168(sc[0][n], a0, bq[n][2 * w][0], bq[n][2 * w][1]);
+                    mma168(sc[0][n], a1, bq[n][2 * w + 1][0], bq[n][2 * w + 1][1]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + g + (e >> 1) * 8;
+                    sc[0][n][e] = j < last && j <= token[n][e & 1] ? sc[0][n][e] * kLog2e : -INFINITY;
+                }
+            uint32_t pb[1][NR][2];
+            softmax(sc, pb, std::integral_constant<int, 1>{});
+            uint4 x[4][D / 64];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = j0 + 2 * t + (k & 1) + 8 * (k >> 1);
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w)
+                    x[k][w] = j < last ? __ldg(reinterpret_cast<const uint4*>(vf + static_cast<int64_t>(j) * kv_stride + g * (D / 8)) + w)
+                                       : make_uint4(0, 0, 0, 0);
+            }
+            // A hidden key's probability is 0, and 0 * infinity would be NaN: infinities and
+            // NaN leave the product and are added for the rows that see them.
+            bool wild = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) wild |= any_wild(x[k][w]);
+            if (__any_sync(0xffffffffu, wild)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) x[k][w] = without_wild(x[k][w]);
+                for (int k = 0; k < 16 && j0 + k < last; ++k) {
+                    const __half* vr = vf + static_cast<int64_t>(j0 + k) * kv_stride + g * (D / 8);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // pb's lane (row, key / 2) holds keys 2t, 2t + 1 and their next 8
+                            const uint32_t w = __shfl_sync(0xffffffffu, k < 8 ? pb[0][n][0] : pb[0][n][1],
+                                                           (2 * t + e) * 4 + ((k & 7) >> 1));
+                            const float pr = (k & 1) ? h2f_hi(w) : h2f_lo(w);
+                            if (j0 + k > token[n][e]) continue;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const float v0 = __half2float(vr[2 * i]), v1 = __half2float(vr[2 * i + 1]);
+                                if (!isfinite(v0)) acc[i][n][e] = fmaf(pr, v0, acc[i][n][e]);
+                                if (!isfinite(v1)) acc[i][n][2 + e] = fmaf(pr, v1, acc[i][n][2 + e]);
+                            }
+                        }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                auto word = [&](int k) {
+                    const uint4& v = x[k][i / 4];
+                    return i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+                };
+                const uint32_t a[4] = {byte_perm(word(0), word(1), 0x5410u), byte_perm(word(0), word(1), 0x7632u),
+                                       byte_perm(word(2), word(3), 0x5410u), byte_perm(word(2), word(3), 0x7632u)};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma168(acc[i][n], a, pb[0][n][0], pb[0][n][1]);
+            }
+        }
+    }
+
+    // ---- cached keys
+    const int kgrp = t * (D / 4) / GS, vgrp = g * (D / 8) / GS;     // group of this lane's dims
+    for (int s = 0; s < stages; ++s) {
+        cp_wait<ST - 2>();
+        __syncwarp();                     // the stage has landed for, and the one before it is read by, every lane
+        if (s + ST - 1 < stages) {
+            const int r = row_next;
+            row_next = s + ST < stages ? row_index(s + ST) : -1;
+            load_stage(s + ST - 1, r);
+        }
+        cp_commit();
+        const int j0 = key0 + s * KEYS + warp * KW;
+        if (j0 >= key1) continue;
+        const unsigned char* st = ring + warp * ST * STAGE + (s % ST) * STAGE;
+        const uint32_t* kmeta = reinterpret_cast<const uint32_t*>(st + 2 * CODE);
+        const uint32_t* vmeta = reinterpret_cast<const uint32_t*>(st + 2 * CODE + META);
+        float sc[KT][NR][4];
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) sc[k][n][0] = sc[k][n][1] = sc[k][n][2] = sc[k][n][3] = 0.f;
+            uint32_t x0[KB / 16], x8[KB / 16];
+            const unsigned char* kc = st + (k * 16 + g) * KB + t * (KB / 4);
+#pragma unroll
+            for (int w = 0; w < KB / 16; w += (KB >= 64 ? 4 : 2)) {
+                if (KB >= 64) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(kc + w * 4), z = *reinterpret_cast<const uint4*>(kc + 8 * KB + w * 4);
+                    x0[w] = a.x; x0[(w + 1) % (KB / 16)] = a.y; x0[(w + 2) % (KB / 16)] = a.z; x0[(w + 3) % (KB / 16)] = a.w;
+                    x8[w] = z.x; x8[(w + 1) % (KB / 16)] = z.y; x8[(w + 2) % (KB / 16)] = z.z; x8[(w + 3) % (KB / 16)] = z.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2*>(kc + w * 4), z = *reinterpret_cast<const uint2*>(kc + 8 * KB + w * 4);
+                    x0[w] = a.x; x0[(w + 1) % (KB / 16)] = a.y;
+                    x8[w] = z.x; x8[(w + 1) % (KB / 16)] = z.y;
+                }
+            }
+            const uint32_t m0 = kmeta[(k * 16 + g) * NG + kgrp], m8 = kmeta[(k * 16 + g + 8) * NG + kgrp];
+            const uint32_t st0 = dup16(step16_of(m0)), st8 = dup16(step16_of(m8)), mn0 = dup_lo(m0), mn8 = dup_lo(m8);
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t a[4], z[4];
+                constexpr int W = BITS / 4;
+                key_pairs<BITS>(a, x0[w * W], x0[w * W + W - 1], st0, mn0);
+                key_pairs<BITS>(z, x8[w * W], x8[w * W + W - 1], st8, mn8);
+                const uint32_t a0[4] = {a[0], z[0], a[1], z[1]}, a1[4] = {a[2], z[2], a[3], z[3]};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    mma168(sc[k][n], a0, bq[n][2 * w][0], bq[n][2 * w][1]);
+                    mma168(sc[k][n], a1, bq[n][2 * w + 1][0], bq[n][2 * w + 1][1]);
+                }
+            }
+            const bool in0 = j0 + k * 16 + g < key1, in8 = j0 + k * 16 + g + 8 < key1;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                sc[k][n][0] = in0 ? sc[k][n][0] * kLog2e : -INFINITY;
+                sc[k][n][1] = in0 ? sc[k][n][1] * kLog2e : -INFINITY;
+                sc[k][n][2] = in8 ? sc[k][n][2] * kLog2e : -INFINITY;
+                sc[k][n][3] = in8 ? sc[k][n][3] * kLog2e : -INFINITY;
+            }
+        }
+        uint32_t pb[KT][NR][2];
+        softmax(sc, pb, std::integral_constant<int, KT>{});
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            constexpr int VW = KB / 32;                    // words a lane takes of a key
+            uint32_t x[4][VW];
+            uint32_t step[2], mn[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int key = k * 16 + 2 * t + 8 * p;
+                const uint32_t ma = vmeta[key * NG + vgrp], mz = vmeta[(key + 1) * NG + vgrp];
+                step[p] = static_cast<uint32_t>(__half_as_ushort(step16_of(ma))) |
+                          (static_cast<uint32_t>(__half_as_ushort(step16_of(mz))) << 16);
+                mn[p] = byte_perm(ma, mz, 0x5410u);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = k * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+                const int off = g * (KB / 8);
+                const unsigned char* vp = st + CODE + value_piece<KB>(key, off / 16) * 16 + off % 16;
+                if (VW == 4) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(vp);
+                    x[i][0] = a.x; x[i][1 % VW] = a.y; x[i][2 % VW] = a.z; x[i][3 % VW] = a.w;
+                } else if (VW == 2) {
+                    const uint2 a = *reinterpret_cast<const uint2*>(vp);
+                    x[i][0] = a.x; x[i][1 % VW] = a.y;
+                } else {
+                    x[i][0] = *reinterpret_cast<const uint32_t*>(vp);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {             // dims 2i and 2i + 1 of this lane's D/8
+                uint32_t a[4];
+                if (BITS == 4) {
+                    constexpr int dummy = 0;
+                    (void)dummy;
+                    const uint32_t sel = (i % 4) * 0x11u + (4 + i % 4) * 0x1100u;
+                    const uint32_t y0 = byte_perm(x[0][i / 4 % VW], x[1][i / 4 % VW], sel);
+                    const uint32_t y1 = byte_perm(x[2][i / 4 % VW], x[3][i / 4 % VW], sel);
+                    a[0] = h2_fma(codes_lo(y0), step[0], mn[0]);
+                    a[1] = h2_fma(codes_hi(y0), step[0], mn[0]);
+                    a[2] = h2_fma(codes_lo(y1), step[1], mn[1]);
+                    a[3] = h2_fma(codes_hi(y1), step[1], mn[1]);
+                } else {
+                    const int w = i / 2 % VW, b0 = (i % 2) * 2;
+                    // bytes b0, b0 + 1 of both keys: [k0.b0, k1.b0, k0.b1, k1.b1]
+                    const uint32_t sel = b0 | ((4u + b0) << 4) | ((1u + b0) << 8) | ((5u + b0) << 12);
+                    const uint32_t y0 = byte_perm(x[0][w], x[1][w], sel), y1 = byte_perm(x[2][w], x[3][w], sel);
+                    a[0] = h2_fma(codes_b01(y0), step[0], mn[0]);
+                    a[1] = h2_fma(codes_b23(y0), step[0], mn[0]);
+                    a[2] = h2_fma(codes_b01(y1), step[1], mn[1]);
+                    a[3] = h2_fma(codes_b23(y1), step[1], mn[1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma168(acc[i][n], a, pb[k][n][0], pb[k][n][1]);
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();                      // every warp is done with the ring, which now takes the outputs
+
+    // ---- join the warps
+    float* so = reinterpret_cast<float*>(ring);            // [4][R][D]
+    __shared__ float sm[4][R], sl[4][R];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float s = l[n][e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+            const int r = n * 8 + 2 * t + e;
+            if (g == 0) {
+                sm[warp][r] = m[n][e];
+                sl[warp][r] = s;
+            }
+            float* dst = so + (warp * R + r) * D + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][n][e], acc[i][n][2 + e]);
+        }
+    __syncthreads();
+    const int tile_id = u.b * most_tiles + u.tile;
+    if (tid == 0 && u.part == 0 && u.parts > 1) {
+        // partial slots of (sequence, tile, part) lie side by side: the tile's first is this block's
+        records[static_cast<int64_t>(tile_id) * plan.heads + head] = TileRecord{u.parts, unit};
+    } else if (tid == 0 && u.part == 0) {
+        records[static_cast<int64_t>(tile_id) * plan.heads + head] = TileRecord{1, 0};
+    }
+    for (int i = tid; i < R * (D / 4); i += 128) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        if (row0 + r >= row_end) continue;
+        float top = -FLT_MAX;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[w][r]);
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = exp2_fast(sm[w][r] - top);
+            const float4 x = *reinterpret_cast<const float4*>(so + (w * R + r) * D + d);
+            sum = fmaf(f, sl[w][r], sum);
+            a.x = fmaf(f, x.x, a.x);
+            a.y = fmaf(f, x.y, a.y);
+            a.z = fmaf(f, x.z, a.z);
+            a.w = fmaf(f, x.w, a.w);
+        }
+        if (u.parts == 1) {
+            const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
+            const int64_t at = static_cast<int64_t>(u.first + tok) * (plan.heads * plan.share) + h;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint2*>(o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+            if (d == 0 && lse) lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        } else {
+            // [unit][head][row][D + 4]: the output, then maximum and sum
+            float* p = parts_ws + ((static_cast<int64_t>(unit) * plan.heads + head) * R + r) * (D + 4);
+            *reinterpret_cast<float4*>(p + d) = a;
+            if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(top, sum);
+        }
+    }
+}
+
+// Joins the parts of one row tile (of R rows) and key head.
+template <int D, int R>
+__global__ void __launch_bounds__(128) paged_join_kernel(PagedView c, RowsOf rows, RowsPlan plan, const float* __restrict__ parts_ws,
+                                                         const TileRecord* __restrict__ records, __half* __restrict__ o,
+                                                         float* __restrict__ lse, int most_tiles, int units) {
+    pdl_wait();
+    pdl_trigger();
+    const int head = blockIdx.x % plan.heads, tile_id = blockIdx.x / plan.heads;
+    const int b = tile_id / most_tiles, row0 = (tile_id % most_tiles) * R;
+    int first;
+    const int row_end = rows_of(rows, b, first, c.status) * plan.share;
+    if (row0 >= row_end) return;
+    const TileRecord rec = records[static_cast<int64_t>(tile_id) * plan.heads + head];
+    // offsets that overlap (cu out of order) can leave a tile without a unit, its record unset
+    if (rec.parts <= 1 || rec.slot < 0 || rec.parts > units || rec.slot > units - rec.parts) return;
+    for (int i = threadIdx.x; i < R * (D / 4); i += 128) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        if (row0 + r >= row_end) break;
+        const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
+        const float* p = parts_ws + ((static_cast<int64_t>(rec.slot) * plan.heads + head) * R + r) * (D + 4);
+        float top = -FLT_MAX;
+        for (int k = 0; k < rec.parts; ++k) top = fmaxf(top, __ldg(p + k * step + D));
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < rec.parts; ++k) {
+            const float2 ml = __ldg(reinterpret_cast<const float2*>(p + k * step + D));
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + k * step + d));
+            const float f = exp2_fast(ml.x - top);
+            sum = fmaf(f, ml.y, sum);
+            a.x = fmaf(f, x.x, a.x);
+            a.y = fmaf(f, x.y, a.y);
+            a.z = fmaf(f, x.z, a.z);
+            a.w = fmaf(f, x.w, a.w);
+        }
+        const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
+        const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+        if (d == 0 && lse) lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+}
+
+// ---- accumulated weights ------------------------------------------------------------------
+//
+// weight[slot] += sum over rows of exp(s - lse): the scores again, now with the rows' final
+// statistics. A warp holds 32 keys as operands in registers and goes through all query
+// rows of the sequence, so every key's sum stays in its lanes and is added in one fixed
+// order; no atomics. Query rows pass through shared memory, 32 at a time, for 4 warps.
+template <int D, int BITS, int GS>
+__global__ void __launch_bounds__(128) paged_weight_kernel(PagedView c, RowsOf rows, RowsPlan plan, const __half* __restrict__ q,
+                                                           int64_t q_stride, const __half* __restrict__ k_new, int64_t kv_stride,
+                                                           const float* __restrict__ lse) {
+    constexpr int KB = D * BITS / 8, NG = D / GS, QR = 32, LD = D + 8;
+    __shared__ __align__(16) __half sq[2][QR * LD];
+    __shared__ float sl[2][QR];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int head = blockIdx.y, b = blockIdx.z;
+    int first;
+    const int n = rows_of(rows, b, first, c.status), ctx = slots_of(c, b), cap = paged_capacity(c);
+    const int old_blocks = (ctx + 127) / 128;
+    const bool fresh = static_cast<int>(blockIdx.x) >= old_blocks;
+    const int j0 = (static_cast<int>(blockIdx.x) - (fresh ? old_blocks : 0)) * 128 + warp * 32;    // slot, or fresh token
+    const int jend = fresh ? (k_new ? n : 0) : ctx;
+    if (j0 - warp * 32 >= jend || n == 0) return;       // a sequence without new tokens keeps its weights
+    int row[4];                                         // pool rows of keys j0 + g + 8 i, -1: none
+    uint32_t a[2][D / 16][4];
+    const int kgrp = t * (D / 4) / GS;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + g + 8 * i, slot = fresh ? ctx + j : j;
+        row[i] = -1;
+        if (j < jend) {
+            if (slot >= cap) {
+                paged_bad(c);
+            } else {
+                const int p = page_of(c, b, slot);
+                if (p >= 0) row[i] = slot_row(c, p, head, slot);
+            }
+        }
+        uint32_t pr[D / 32][4];
+        if (!fresh) {
+            const int64_t r = row[i] < 0 ? 0 : row[i];
+            const uint32_t meta = row[i] < 0 ? 0u : __ldg(c.km + r * NG + kgrp);
+            const uint32_t step = dup16(step16_of(meta)), mn = dup_lo(meta);
+            const uint8_t* kc = c.kc + r * KB + t * (KB / 4);
+            uint32_t x[KB / 16];
+#pragma unroll
+            for (int w = 0; w < KB / 16; w += 2) {
+                const uint2 v = row[i] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(kc + w * 4));
+                x[w] = v.x;
+                x[w + 1] = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) key_pairs<BITS>(pr[w], x[w * (BITS / 4)], x[w * (BITS / 4) + BITS / 4 - 1], step, mn);
+        } else {
+            const uint4* x = reinterpret_cast<const uint4*>(k_new + static_cast<int64_t>(first + (j < jend ? j : 0)) * kv_stride +
+                                                            head * D + t * (D / 4));
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) key_pairs_fresh<BITS>(pr[w], j < jend ? __ldg(x + w) : make_uint4(0, 0, 0, 0));
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            a[i / 2][2 * w][i % 2] = pr[w][0];
+            a[i / 2][2 * w][2 + i % 2] = pr[w][1];
+            a[i / 2][2 * w + 1][i % 2] = pr[w][2];
+            a[i / 2][2 * w + 1][2 + i % 2] = pr[w][3];
+        }
+    }
+    // rows of the tokens that see any of the block's keys
+    const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
+    const int tiles = (row_end - row_lo + QR - 1) / QR;
+    auto load_rows = [&](int s) {
+        for (int i = tid; i < QR * (D / 8); i += 128) {
+            const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
+            const bool ok = r < row_end;
+            const int tok = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
+            cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
+        }
+        if (tid < QR) {
+            const int r = row_lo + s * QR + tid;
+            const int tok = r / plan.share, h = head * plan.share + r % plan.share;
+            sl[s & 1][tid] = r < row_end ? __ldg(lse + static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h) * kLog2e : INFINITY;
+        }
+        cp_commit();
+    };
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    load_rows(0);
+    for (int s = 0; s < tiles; ++s) {
+        if (s + 1 < tiles)
+            load_rows(s + 1);
+        else
+            cp_commit();
+        cp_wait<1>();
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < QR / 8; ++u) {
+            const int r0 = row_lo + s * QR + u * 8;
+            if (r0 >= row_end) break;
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const __half* qr = &sq[s & 1][(u * 8 + g) * LD + t * (D / 4)];
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t z[4];
+                key_pairs_fresh<BITS>(z, *reinterpret_cast<const uint4*>(qr + w * 8));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mma168(sc[k], a[k][2 * w], z[0], z[1]);
+                    mma168(sc[k], a[k][2 * w + 1], z[2], z[3]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 2 * t + e;
+                const float lr = sl[s & 1][u * 8 + 2 * t + e];      // +inf behind the last row: no weight
+                const int tok = fresh ? r / plan.share : INT32_MAX;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const float p = exp2_fast(fmaf(sc[k][2 * hh + e], kLog2e, -lr));
+                        const int j = j0 + k * 16 + hh * 8 + g;
+                        sum[2 * k + hh] += j <= tok ? p : 0.f;
+                    }
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        if (t == 0 && row[i] >= 0) c.weight[row[i]] = fresh ? sum[i] : c.weight[row[i]] + sum[i];
+    }
+}
+
+// ---- host -----------------------------------------------------------------------------------
+
+struct AttnPlan {
+    int share, row_tile, most_tiles, target;
+    int64_t units, records_bytes, parts_bytes, lse_bytes;
+    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes; }
+};
+
+inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total, int most, bool accumulate) {
+    AttnPlan p{};
+    p.share = n_heads / c->n_kv_heads;
+    p.row_tile = static_cast<int64_t>(most) * p.share <= 8 ? 8 : 16;
+    p.most_tiles = static_cast<int>((static_cast<int64_t>(most) * p.share + p.row_tile - 1) / p.row_tile);
+    // blocks wanted on the device at once: 4 a multiprocessor
+    p.target = 4 * sm_count();
+    // every sequence's row tiles, and what their parts add: at most target blocks over all heads
+    const int64_t tiles = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch;
+    p.units = tiles + (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
+    p.records_bytes = up256(static_cast<int64_t>(batch) * p.most_tiles * c->n_kv_heads * sizeof(TileRecord));
+    p.parts_bytes = up256(p.units * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
+    p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
+    return p;
+}
+
+}  // namespace
+}  // namespace flexq
+
+using namespace flexq;
+
+namespace {
+
+int validate_attention(const flex_paged_cache* c, int32_t n_heads, int32_t accumulate) {
+    const int rc = validate_paged(c, true);
+    if (rc != FLEX_OK) return rc;
+    FLEX_REQUIRE(n_heads > 0 && n_heads % c->n_kv_heads == 0, FLEX_ERR_INVALID_ARG);
+    FLEX_REQUIRE(n_heads <= 65535, FLEX_ERR_UNSUPPORTED);
+    FLEX_REQUIRE(!accumulate || c->weight, FLEX_ERR_INVALID_ARG);
+    return FLEX_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t flex_paged_attention_ws_bytes(const flex_paged_cache* cache, int32_t n_heads, int32_t batch, int32_t total,
+                                                 int32_t most, int32_t accumulate) {
+    int rc = validate_attention(cache, n_heads, accumulate);
+    if (rc != FLEX_OK) return rc;
+    FLEX_REQUIRE(batch > 0 && batch <= cache->batch && total >= 0 && most >= 0, FLEX_ERR_INVALID_ARG);
+    FLEX_REQUIRE(most <= (1 << 24), FLEX_ERR_UNSUPPORTED);
+    return attn_plan(cache, n_heads, batch, total, most, accumulate != 0).bytes();
+}
+
+extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q, int64_t q_stride, int32_t n_heads,
+                                    const void* k_new, const void* v_new, int64_t kv_stride, void* o, float* lse,
+                                    const int32_t* cu_new, int32_t batch, int32_t total, int32_t most, int32_t accumulate,
+                                    void* ws, int64_t ws_bytes, void* stream) {
+    int rc = validate_attention(cache, n_heads, accumulate);
+    if (rc == FLEX_OK) rc = validate_rows(cache, cu_new, batch, total, most);
+    if (rc != FLEX_OK) return rc;
+    FLEX_REQUIRE(q && o && (k_new == nullptr) == (v_new == nullptr), FLEX_ERR_INVALID_ARG);
+    FLEX_REQUIRE(q_stride >= static_cast<int64_t>(n_heads) * cache->head_dim, FLEX_ERR_INVALID_ARG);
+    FLEX_REQUIRE(k_new == nullptr || kv_stride >= static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim,
+                 FLEX_ERR_INVALID_ARG);
+    FLEX_REQUIRE(q_stride % 8 == 0 && (k_new == nullptr || kv_stride % 8 == 0), FLEX_ERR_ALIGN);
+    FLEX_REQUIRE(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(o), FLEX_ERR_ALIGN);
+    FLEX_REQUIRE((reinterpret_cast<uintptr_t>(lse) & 3u) == 0, FLEX_ERR_ALIGN);
+    const AttnPlan p = attn_plan(cache, n_heads, batch, total, most, accumulate != 0);
+    FLEX_REQUIRE(ws != nullptr && ws_bytes >= p.bytes(), FLEX_ERR_WORKSPACE);
+    FLEX_REQUIRE(aligned16(ws), FLEX_ERR_ALIGN);
+    if (most == 0 || total == 0) return FLEX_OK;
+    const int kvh = cache->n_kv_heads;
+    FLEX_REQUIRE(p.units * kvh < (1LL << 31) && static_cast<int64_t>(batch) * p.most_tiles * kvh < (1LL << 31),
+                 FLEX_ERR_UNSUPPORTED);
+    FLEX_REQUIRE(static_cast<int64_t>(most) * p.share < (1LL << 31), FLEX_ERR_UNSUPPORTED);
+
+    const PagedView view = paged_view(cache);
+    const RowsOf rows{cu_new, most, total};
+    const RowsPlan plan{batch, p.share, p.target, kvh};
+    const cudaStream_t st = as_stream(stream);
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    TileRecord* records = reinterpret_cast<TileRecord*>(w);
+    float* parts = reinterpret_cast<float*>(w + p.records_bytes);
+    if (lse == nullptr && accumulate) lse = reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes);
+    const __half* qh = static_cast<const __half*>(q);
+    const __half* kn = static_cast<const __half*>(k_new);
+    const __half* vn = static_cast<const __half*>(v_new);
+    __half* oh = static_cast<__half*>(o);
+    const dim3 grid(static_cast<unsigned>(p.units * kvh)), join(static_cast<unsigned>(static_cast<int64_t>(batch) * p.most_tiles * kvh));
+    const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;
+#define ROWS(D_, B_, G_, N_)                                                                                        \
+    do {                                                                                                            \
+        constexpr int ring = RowsShape<D_, B_>::STAGES * 4 * RowsShape<D_, B_>::KW * 2 * (RowsShape<D_, B_>::KB + D_ / G_ * 4); \
+        constexpr int outs = 4 * 8 * N_ * D_ * 4, smem = ring > outs ? ring : outs;                                 \
+        set_smem_once(paged_rows_kernel<D_, B_, G_, N_>, smem);                                                     \
+        launch_k(paged_rows_kernel<D_, B_, G_, N_>, grid, dim3(128), smem, st, true, view, rows, plan, qh, q_stride, kn, vn, \
+                 kv_stride, oh, lse, parts, records, p.most_tiles);                                                 \
+        launch_k(paged_join_kernel<D_, 8 * N_>, join, dim3(128), 0, st, true, view, rows, plan,                     \
+                 static_cast<const float*>(parts), static_cast<const TileRecord*>(records), oh, lse, p.most_tiles, \
+                 static_cast<int>(p.units));                                                                        \
+    } while (0)
+#define ROWS_N(D_, B_, G_) \
+    do { if (p.row_tile == 8) ROWS(D_, B_, G_, 1); else ROWS(D_, B_, G_, 2); } while (0)
+    if (D == 64) {
+        if (B == 4 && G == 32) ROWS_N(64, 4, 32); else if (B == 4) ROWS_N(64, 4, 64);
+        else if (G == 32) ROWS_N(64, 8, 32); else ROWS_N(64, 8, 64);
+    } else {
+        if (B == 4 && G == 32) ROWS_N(128, 4, 32); else if (B == 4) ROWS_N(128, 4, 64);
+        else if (G == 32) ROWS_N(128, 8, 32); else ROWS_N(128, 8, 64);
+    }
+#undef ROWS_N
+#undef ROWS
+    if (accumulate) {
+        const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
+        // every 128 slots, and 128 fresh tokens; blocks behind a sequence's end return at once
+        const dim3 wgrid(static_cast<unsigned>((cap + 127) / 128 + (k_new ? (most + 127) / 128 : 0)), kvh, batch);
+#define WEIGHT(D_, B_, G_)                                                                                       \
+    launch_k(paged_weight_kernel<D_, B_, G_>, wgrid, dim3(128), 0, st, true, view, rows, plan, qh, q_stride, kn, kv_stride, \
+             static_cast<const float*>(lse))
+        if (D == 64) {
+            if (B == 4 && G == 32) WEIGHT(64, 4, 32); else if (B == 4) WEIGHT(64, 4, 64);
+            else if (G == 32) WEIGHT(64, 8, 32); else WEIGHT(64, 8, 64);
+        } else {
+            if (B == 4 && G == 32) WEIGHT(128, 4, 32); else if (B == 4) WEIGHT(128, 4, 64);
+            else if (G == 32) WEIGHT(128, 8, 32); else WEIGHT(128, 8, 64);
+        }
+#undef WEIGHT
+    }
+    return launch_status();
+}

@@ -322,6 +322,102 @@ int flex_dequant_gemm(const void* x, const flexq_tensor* W, const void* bias,
 int flex_layernorm(const void* x, const void* g, const void* b, void* y, int64_t rows,
                    int32_t h, void* stream);
 
+/* ---- paged compressed KV cache ------------------------------------------------ */
+/* The pages' KV cache (section 6.3: 4 bits, group 64 along the head dimension) for a ragged
+ * batch: sequences of different lengths share one pool of pages; heads of queries may
+ * share a key head; a piece of a prompt attends to what earlier pieces stored; and a
+ * bounded cache gives slots up by accumulated attention weight. The order of one step is
+ * the pages' load_cache, compute_layer, store_cache: attention reads the cached slots and
+ * the new tokens' own fresh fp16 keys/values, then the new tokens are stored.
+ *
+ *   k_codes, v_codes: uint8 [num_pages][n_kv_heads][page_size][head_dim*bits/8]
+ *   k_meta,  v_meta : half2 [num_pages][n_kv_heads][page_size][head_dim/group_size]
+ *   weight  : NULL or fp32 [num_pages][n_kv_heads][page_size], each slot's accumulated
+ *             attention weight (flex_paged_attention with accumulate, flex_paged_evict).
+ *   slot_pos: NULL or int32 [num_pages][n_kv_heads][page_size], the position of the token
+ *             in each slot (written by flex_paged_store_kv, used by flex_paged_evict).
+ *   page_table: device int32 [batch][max_pages]; slot s of sequence b is slot
+ *             s % page_size of page page_table[b][s / page_size]. Entries behind a
+ *             sequence's last page are not read. Two sequences may share pages that no
+ *             call writes.
+ *   ctx_len : device int32 [batch], slots that each sequence holds before the call. No call
+ *             changes it (the layers of a model share it): the caller adds the new tokens,
+ *             or takes flex_paged_evict's new_len, once every layer is done.
+ *   page_size a power of two, 16..1024; head_dim 64 or 128; cfg as in flex_kv_cache;
+ *   max_pages*page_size <= 2^30, num_pages*page_size*n_kv_heads < 2^31.
+ *
+ * The new rows of a ragged batch: sequence b's are rows [cu[b], cu[b+1]) of the call's row
+ * tensors, cu a device int32 [batch + 1]; `most` bounds the rows of one sequence, `total`
+ * those of all. cu NULL: `most` rows each, total == batch * most. Rows that no sequence
+ * has are neither read nor written. All lengths and tables are read on the device, so a
+ * captured call may be replayed with other contents.
+ *
+ * What only the device can see - a page id outside [0, num_pages), ctx_len outside
+ * [0, max_pages*page_size], cu that decreases or exceeds most or total, a new slot behind
+ * the table - is reported as FLEX_ERR_INVALID_ARG by flex_get_status; the sequence or
+ * slot concerned is skipped or its results are unspecified, all others are right.        */
+typedef struct {
+    void *k_codes, *k_meta, *v_codes, *v_meta;
+    float* weight;
+    int32_t* slot_pos;
+    const int32_t* page_table;
+    const int32_t* ctx_len;
+    int32_t num_pages, page_size, max_pages, batch, n_kv_heads, head_dim;
+    flexq_config cfg;
+} flex_paged_cache;
+
+/* store_cache for new tokens: row r of sequence b (its i-th, i = r - cu[b]) goes to slot
+ * ctx_len[b] + i, quantised like flexq_compress along the head dimension. k_new, v_new:
+ * fp16 rows of `row_stride` elements (a multiple of 8), head h at h*head_dim. slot_pos (if
+ * not NULL) takes pos0[b] + i; pos0: device int32 [batch], or NULL for ctx_len. */
+int flex_paged_store_kv(const flex_paged_cache* cache, const void* k_new, const void* v_new, int64_t row_stride,
+                        const int32_t* cu_new, int32_t batch, int32_t total, int32_t most, const int32_t* pos0,
+                        void* stream);
+
+/* load_cache into rows: row cu[b] + i takes the dequantised slot start[b] + i (start: device
+ * int32 [batch], NULL for 0), with flexq_decompress's values. Layout as in the store. */
+int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, void* v_out, int64_t row_stride,
+                       const int32_t* cu_rows, int32_t batch, int32_t total, int32_t most, const int32_t* start,
+                       void* stream);
+
+/* Attention of new tokens over the cache. q: fp16 rows of q_stride elements, n_heads heads
+ * (a multiple of n_kv_heads; heads [g*s, g*s + s), s = n_heads / n_kv_heads, share key head
+ * g), used as given (callers pre-scale). k_new, v_new: fp16 rows of kv_stride elements,
+ * n_kv_heads heads: the new tokens' own keys/values.
+ *   Token i of sequence b attends to slots [0, ctx_len[b]) and to fresh tokens 0..i.
+ *   k_new == v_new == NULL: cross attention, to the slots alone (an encoder's states of
+ *   another length, stored once); a token without any slot gets zeros.
+ *   A code stands for fp16(c * fp16(1/scale) + min), one fused fp16 multiply-add, as in
+ *   flex_dequant_gemm (a constant group for min).
+ * o: fp16 [total][n_heads*head_dim]. lse: fp32 [total][n_heads], the logarithm of the sum
+ * of exponentials (-infinity where nothing is attended), or NULL.
+ * accumulate != 0 (needs cache->weight): with p the attention probabilities,
+ *   weight[slot] = (slot < ctx_len ? weight[slot] : 0) + sum of p over the sequence's new
+ *   tokens and the heads that share the key head, for the slots [0, ctx_len + new tokens)
+ *   (cross attention: [0, ctx_len)). Each slot's sum has a fixed order.
+ * ws: flex_paged_attention_ws_bytes(...) bytes, nothing in it has to be set; calls that may
+ * run at the same time need workspaces of their own. Strides are multiples of 8. */
+int64_t flex_paged_attention_ws_bytes(const flex_paged_cache* cache, int32_t n_heads, int32_t batch, int32_t total,
+                                      int32_t most, int32_t accumulate);
+int flex_paged_attention(const flex_paged_cache* cache, const void* q, int64_t q_stride, int32_t n_heads,
+                         const void* k_new, const void* v_new, int64_t kv_stride, void* o, float* lse,
+                         const int32_t* cu_new, int32_t batch, int32_t total, int32_t most, int32_t accumulate,
+                         void* ws, int64_t ws_bytes, void* stream);
+
+/* Eviction: where sequence b (every b < cache->batch) holds more than `budget` slots, each
+ * key head keeps `budget` of them: first the slots with slot_pos > (the head's largest) -
+ * recent, then those of the largest weight; equal weights go to the lower slot, a NaN
+ * counts as -infinity. The i-th slot below the budget that is given up takes codes,
+ * metadata, weight and position of the i-th kept slot behind it; nothing else moves, and
+ * slots from the budget on keep their old contents. new_len[b] = min(ctx_len[b], budget)
+ * (device int32 [batch], not overlapping ctx_len). 0 <= recent <= budget, budget > 0.
+ * Needs weight and slot_pos. A page must belong to one sequence only. Heads hold
+ * different tokens afterwards, in no order: attention over the cache needs none.
+ * ws: flex_paged_evict_ws_bytes(cache, budget) bytes, as for the attention. */
+int64_t flex_paged_evict_ws_bytes(const flex_paged_cache* cache, int32_t budget);
+int flex_paged_evict(const flex_paged_cache* cache, int32_t budget, int32_t recent, int32_t* new_len, void* ws,
+                     int64_t ws_bytes, void* stream);
+
 /* ---- status ------------------------------------------------------------------ */
 
 /* Synchronises `stream`, then returns and clears the device status word of the
@@ -350,7 +446,7 @@ uint64_t flex_set_wait_limit_ns(uint64_t ns);
 const int32_t* flex_set_gemm_gate(const int32_t* gate);
 
 /* Layout of the ABI structs as this library was compiled: which = 0 flexq_config,
- * 1 flexq_tensor, 2 flex_layer, 3 flex_kv_cache; field = -1 returns sizeof, field = i
+ * 1 flexq_tensor, 2 flex_layer, 3 flex_kv_cache, 4 flex_paged_cache; field = -1 returns sizeof, field = i
  * the byte offset of the struct's i-th field (declaration order). -1 if out of range.
  * Bindings compare these with their own declarations before any call. */
 int64_t flex_abi_layout(int32_t which, int32_t field);

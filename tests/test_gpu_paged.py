@@ -1,0 +1,628 @@
+"""Parity of the paged KV cache's store, load, attention and eviction with the float64
+oracle, at the sizes and masks where they can go wrong, one after the other as a serving
+step uses them, captured and replayed, and with what only the device can refuse.
+
+Tolerances, with u = 2^-11 (half a step of fp16) and e = 2^-24 (of fp32):
+  a score is a sum of head_dim exact products in fp32: at most (head_dim + 4) e times the sum
+  of their magnitudes `size`, the factor log2 e and the subtraction of the maximum among
+  them; one exponential is within 2^-21 of its value. So a probability is off by
+      ep = 2 (head_dim + 4) e size + 2^-21, relative,
+  the log-sum-exp by ep + keys e + 2 e |lse|, an accumulated weight by (2 ep + rows e) of what
+  was added and e of the whole (both statistics and score enter).
+  The output: probabilities rounded to fp16 (u, and 2^-25 where they underflow, against a
+  largest one of 1), sums of `keys` terms, and one rounding: u |o| + (u + 2 ep + keys e)
+  max|v| + keys 2^-25 max|v|."""
+import numpy as np
+import pytest
+import torch
+
+import group_wise_int4_b200 as fq
+from oracle.paged import PagedCache
+from _helpers import sync_status, to_np
+
+pytestmark = pytest.mark.gpu
+
+U, E = 2.0 ** -11, 2.0 ** -24
+TAIL = 2
+
+
+class Case:
+    """A cache on the device and the oracle's, filled through the device's own store."""
+
+    def __init__(self, seed, ctx, heads=2, dim=64, bits=4, group=32, page=16, room=0, weights=True, spare=2):
+        r = self.r = np.random.default_rng(seed)
+        self.heads, self.dim, self.bits, self.group, self.page = heads, dim, bits, group, page
+        per = [max(1, -(-(n + room) // page)) for n in ctx]
+        pages = sum(per) + spare
+        ids = r.permutation(pages)
+        table = np.full((len(ctx), max(per)), -1, np.int32)
+        at = 0
+        for b, n in enumerate(per):
+            table[b, :n] = ids[at:at + n]
+            at += n
+        self.ref = PagedCache(table, np.zeros(len(ctx), np.int32), pages, page, heads, dim, bits, group)
+        self.ctx = torch.zeros(len(ctx), dtype=torch.int32, device="cuda")
+        self.cache = fq.FlexPagedCache(torch.from_numpy(table).cuda(), self.ctx, pages, page, heads, dim, bits, group,
+                                       weight=weights or None, slot_pos=weights or None)
+        for t in (self.cache.k_codes, self.cache.v_codes):
+            t.fill_(0xA5)                                  # what no call writes is not zero
+        for t in (self.cache.k_meta, self.cache.v_meta):
+            t.fill_(float("nan"))
+        self.level = r.standard_normal((heads, dim))
+        if sum(ctx):
+            self.store([self.rows(n) for n in ctx], [self.rows(n) for n in ctx], advance=True)
+
+    def rows(self, n, heads=None):
+        h = heads or self.heads
+        return (self.r.standard_normal((n, h, self.dim)) + self.level[np.arange(h) % self.heads]).astype(np.float16)
+
+    def ragged(self, parts):
+        """Rows of every sequence -> a strided device tensor with rows behind the last one, and offsets."""
+        width = int(np.prod(parts[0].shape[1:]))
+        flat = np.concatenate([x.reshape(len(x), width) for x in parts] + [np.full((TAIL, width), 7.5, np.float16)])
+        wide = torch.full((len(flat), flat.shape[1] + 24), 9.0, dtype=torch.float16, device="cuda")
+        wide[:, 8:8 + flat.shape[1]] = torch.from_numpy(flat).cuda()
+        cu = np.concatenate([[0], np.cumsum([len(x) for x in parts])]).astype(np.int32)
+        return wide[:, 8:], torch.from_numpy(cu).cuda(), int(cu[-1]), max(len(x) for x in parts)
+
+    def set_ctx(self, lens):
+        self.ref.ctx = np.asarray(lens).copy()
+        self.ctx.copy_(torch.as_tensor(np.asarray(lens), dtype=torch.int32))
+
+    def store(self, k, v, advance=False, pos0=None):
+        kd, cu, total, most = self.ragged(k)
+        vd = self.ragged(v)[0]
+        p = None if pos0 is None else torch.as_tensor(pos0, dtype=torch.int32, device="cuda")
+        fq.flex_paged_store_kv(self.cache, kd, vd, kd.stride(0), cu, most, pos0=p, total=total)
+        for b in range(len(k)):
+            self.ref.store(b, k[b], v[b], None if pos0 is None else int(pos0[b]))
+        if advance:
+            self.set_ctx([n + len(x) for n, x in zip(self.ref.ctx, k)])
+
+    def slots(self, pool, b, n):
+        """[heads][n]... of the device's pool."""
+        t = to_np(pool)
+        return np.stack([t[self.ref.at(b, j)[0], :, self.ref.at(b, j)[1]] for j in range(n)], 1) if n else None
+
+    def check_slots(self, what="", weights=False, tol=None):
+        for b, n in enumerate(self.ref.ctx):
+            for name in "kv":
+                for i in range(int(n)):
+                    p, s = self.ref.at(b, i)
+                    got = to_np(getattr(self.cache, name + "_codes")[p, :, s])
+                    assert np.array_equal(got, self.ref.codes[name][p, :, s]), (what, name, b, i)
+                    got = to_np(getattr(self.cache, name + "_meta")[p, :, s]).view(np.uint16)
+                    assert np.array_equal(got, self.ref.meta[name][p, :, s].view(np.uint16)), (what, name, b, i)
+            if self.cache.slot_pos is not None:
+                for i in range(int(n)):
+                    p, s = self.ref.at(b, i)
+                    assert np.array_equal(to_np(self.cache.slot_pos[p, :, s]), self.ref.pos[p, :, s]), (what, b, i)
+
+    def attend(self, q, k=None, v=None, accumulate=False, lse=True, check=True, ws=None, stream=None):
+        nq = q[0].shape[1]
+        qd, cu, total, most = self.ragged(q)
+        o = torch.full((total + TAIL, nq * self.dim), 3.25, dtype=torch.float16, device="cuda")
+        ls = torch.full((total + TAIL, nq), 3.25, device="cuda") if lse else None
+        kd, vd, ks = None, None, 0
+        if k is not None:
+            kd, vd = self.ragged(k)[0], self.ragged(v)[0]
+            ks = kd.stride(0)
+        if ws is None:
+            ws = torch.full((fq.flex_paged_attention_ws_bytes(self.cache, nq, total, most, accumulate, batch=len(q)),), 0xFF,
+                            dtype=torch.uint8, device="cuda")
+        before = self.cache.weight.clone() if accumulate else None
+        fq.flex_paged_attention(self.cache, qd, qd.stride(0), nq, kd, vd, ks, o, ls, cu, most, ws, accumulate=accumulate,
+                                total=total, stream=stream)
+        sync_status()
+        assert bool((o[total:] == 3.25).all()) and (ls is None or bool((ls[total:] == 3.25).all())), "rows behind the last"
+        if check:
+            self.check_attention(q, k, v, o, ls, before)
+        return o, ls
+
+    def check_attention(self, q, k, v, o, ls, before=None):
+        o, ls = to_np(o).astype(np.float64), None if ls is None else to_np(ls).astype(np.float64)
+        at = 0
+        for b in range(len(q)):
+            n, nq = q[b].shape[:2]
+            ro, rl, sums, size = self.ref.attend(b, q[b], None if k is None else k[b], None if v is None else v[b])
+            got = o[at:at + n].reshape(n, nq, self.dim)
+            keys = sums.shape[1]
+            ep = 2 * (self.dim + 4) * E * size + 2.0 ** -21
+            vmax = max([np.abs(self.ref.values("v", b, g)).max(initial=0) for g in range(self.heads)] +
+                       ([] if v is None else [np.abs(v[b].astype(np.float64)).max(initial=0)]))
+            tol = U * np.abs(ro) + (U + 2 * ep + keys * (E + 2.0 ** -25))[..., None] * vmax
+            err = np.abs(got - ro)
+            assert np.all(err <= tol), (b, np.unravel_index(np.argmax(err - tol), err.shape), (err - tol).max())
+            if ls is not None:
+                lt = ls[at:at + n]
+                some = np.isfinite(rl)
+                assert np.array_equal(np.isfinite(lt), some) and np.all(lt[~some] == -np.inf)
+                bound = ep + keys * E + 2 * E * np.abs(np.where(some, rl, 0))
+                assert np.all(np.abs(lt[some] - rl[some]) <= bound[some]), b
+            if before is not None and n:
+                grown = int(self.ref.ctx[b]) + (0 if k is None else n)
+                old = self.slots(before, b, grown)
+                new = self.slots(self.cache.weight, b, grown)
+                if old is not None:
+                    old = old.astype(np.float64)
+                    old[:, int(self.ref.ctx[b]):] = 0
+                    want = old + sums
+                    rows = n * nq // self.heads
+                    bound = (2 * ep.max(initial=0) + keys * E + rows * E + 4 * E) * sums + 2 * E * np.abs(want) + 1e-30
+                    assert np.all(np.abs(new - want) <= bound), (b, np.abs(new - want).max())
+            at += n
+
+
+def _scaled(c, n, heads):
+    return [(x * c.dim ** -0.5).astype(np.float16) for x in (c.rows(m, heads) for m in n)]
+
+
+SHAPES = [(64, 4, 32, 16), (64, 4, 64, 32), (64, 8, 32, 64), (64, 8, 64, 16), (128, 4, 32, 128), (128, 4, 64, 16),
+          (128, 8, 32, 32), (128, 8, 64, 1024)]
+
+
+@pytest.mark.parametrize("dim,bits,group,page", SHAPES)
+def test_store_and_load(dim, bits, group, page):
+    c = Case(1, [0, 17, 33, 1], heads=3, dim=dim, bits=bits, group=group, page=page, room=40)
+    c.check_slots("filled")
+    n = [5, 0, 1, 39]
+    k, v = [c.rows(m) for m in n], [c.rows(m) for m in n]
+    k[0][1, 0, :group] = 0.5                       # a constant group
+    k[3][2, 1, :group] = -0.0
+    v[0][3] *= np.float16(300)
+    c.store(k, v, advance=True, pos0=[100, 7, 2 ** 20, 0])
+    sync_status()
+    c.check_slots("added")
+    # every slot's value, as the codec gives it; rows behind the last one stay
+    start, count = [0, 3, 16, 39], [5, 14, 18, 1]
+    outs = [torch.full((sum(count) + TAIL, 3 * dim + 8), 5.0, dtype=torch.float16, device="cuda") for _ in "kv"]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(count)]), dtype=torch.int32, device="cuda")
+    fq.flex_paged_load_kv(c.cache, outs[0], outs[1], 3 * dim + 8, cu, max(count), total=sum(count),
+                          start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+    sync_status()
+    at = 0
+    for b in range(4):
+        for x, ref in zip(outs, c.ref.load(b, start[b], count[b])):
+            got = to_np(x[at:at + count[b], :3 * dim]).reshape(count[b], 3, dim)
+            assert np.array_equal(got.view(np.uint16), ref.view(np.uint16)), b
+        at += count[b]
+    for x in outs:
+        assert bool((x[at:] == 5).all()) and bool((x[:, 3 * dim:] == 5).all())
+
+
+def test_store_equal_counts_without_offsets():
+    c = Case(2, [3, 20], room=8)
+    k, v = [c.rows(4), c.rows(4)], [c.rows(4), c.rows(4)]
+    kd, vd = (torch.from_numpy(np.concatenate(x).reshape(8, -1)).cuda() for x in (k, v))
+    fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), None, 4)
+    for b in range(2):
+        c.ref.store(b, k[b], v[b])
+    c.set_ctx([7, 24])
+    sync_status()
+    c.check_slots()
+
+
+@pytest.mark.parametrize("dim,bits,group,page", SHAPES)
+@pytest.mark.parametrize("share", [1, 4])
+def test_one_token(dim, bits, group, page, share):
+    ctx = [0, 1, 15, 16, 127, 128, 129, 300]
+    c = Case(3, ctx, heads=3, dim=dim, bits=bits, group=group, page=page, room=1)
+    n = [1] * len(ctx)
+    c.attend(_scaled(c, n, 3 * share), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+@pytest.mark.parametrize("dim,bits,group,page", SHAPES)
+@pytest.mark.parametrize("share", [1, 3])
+def test_chunks(dim, bits, group, page, share):
+    ctx, n = [0, 5, 64, 200, 131, 17], [40, 1, 0, 19, 130, 7]
+    c = Case(4, ctx, heads=2, dim=dim, bits=bits, group=group, page=page, room=130)
+    c.attend(_scaled(c, n, 2 * share), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+@pytest.mark.parametrize("dim,bits,group,page", SHAPES)
+@pytest.mark.parametrize("n", [[1, 1, 1, 1], [3, 129, 0, 64]])
+def test_cross(dim, bits, group, page, n):
+    c = Case(5, [0, 130, 33, 64], heads=2, dim=dim, bits=bits, group=group, page=page)
+    c.attend(_scaled(c, n, 4), accumulate=True)
+
+
+def test_one_long_sequence_is_split():
+    """Few rows over long histories: parts of one sequence's keys are joined."""
+    c = Case(6, [5000, 3, 2100], heads=1, dim=64, bits=4, group=64, page=64, room=4)
+    for n in ([1, 1, 1], [4, 2, 3]):
+        c.attend(_scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+def test_many_sequences():
+    ctx = [(7 * i) % 61 for i in range(70)]
+    c = Case(7, ctx, heads=1, page=16, room=3)
+    n = [i % 4 for i in range(70)]
+    c.attend(_scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+def test_without_lse_and_weights():
+    c = Case(8, [30, 200], weights=False)
+    q, k, v = _scaled(c, [1, 1], 2), [c.rows(1), c.rows(1)], [c.rows(1), c.rows(1)]
+    o, _ = c.attend(q, k, v, lse=False)
+    o2, _ = c.attend(q, k, v)
+    assert torch.equal(o, o2)
+
+
+def test_weights_without_lse_output():
+    c = Case(9, [30, 200], room=9)
+    n = [9, 2]
+    c.attend(_scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True, lse=False)
+
+
+def test_large_scores():
+    """Scores of several thousand, of both signs: the running maximum moves, nothing overflows."""
+    c = Case(10, [100, 40, 3], dim=64, room=20)
+    for n in ([1, 1, 1], [20, 3, 1]):
+        q = [(x * np.float16(60)) for x in (c.rows(m, 2) for m in n)]
+        c.attend(q, [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+@pytest.mark.parametrize("bits,dim", [(4, 64), (4, 128), (8, 64), (8, 128)])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_hidden_tokens_do_not_reach_earlier_rows(bits, dim, bad):
+    """A later token's key and value are not seen by earlier rows, whatever they hold."""
+    c = Case(11, [20, 0], dim=dim, bits=bits, room=40)
+    n = [40, 21]
+    q, k, v = _scaled(c, n, 4), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    o, ls = c.attend(q, k, v)
+    k2, v2 = [x.copy() for x in k], [x.copy() for x in v]
+    k2[0][33, 1, 5], v2[0][33, 0, 7] = bad, bad
+    v2[1][20] = bad
+    o2, ls2 = c.attend(q, k2, v2, check=False)
+    assert torch.equal(o[:33], o2[:33]) and torch.equal(ls[:33], ls2[:33])
+    assert torch.equal(o[40:60], o2[40:60])
+    got = to_np(o2).reshape(-1, 4, dim)
+    # head pair 0 sees the bad value in dim 7 only, head pair 1 the bad key everywhere
+    assert not np.isfinite(got[33:40, :2, 7].astype(np.float64)).any()
+    keep = np.delete(np.arange(dim), 7)
+    assert np.isfinite(got[33:40, :2][..., keep].astype(np.float64)).all()
+    assert not np.isfinite(got[60].astype(np.float64)).any()
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_slots_behind_the_last_are_not_read(one):
+    """The page a sequence ends in holds NaN metadata behind its last slot (Case fills it)."""
+    c = Case(12, [1, 18, 129], dim=128, bits=8, page=64)
+    n = [1, 1, 1] if one else [30, 2, 17]
+    o, ls = c.attend(_scaled(c, n, 2))
+    assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(ls).all())
+
+
+def test_results_repeat():
+    """The same call gives the same bits, weights too: no sum's order depends on timing."""
+    c = Case(13, [900, 40, 0], heads=2, dim=64, room=33)
+    n = [33, 1, 9]
+    q, k, v = _scaled(c, n, 4), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    c.cache.weight.zero_()
+    first = c.attend(q, k, v, accumulate=True, check=False)
+    w = c.cache.weight.clone()
+    for _ in range(3):
+        c.cache.weight.zero_()
+        again = c.attend(q, k, v, accumulate=True, check=False)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]) and torch.equal(w, c.cache.weight)
+
+
+def test_two_streams_with_their_own_workspaces():
+    c = Case(14, [1500, 3, 700], heads=2, room=40)
+    calls = []
+    for n in ([1, 1, 1], [40, 5, 17]):
+        q, k, v = _scaled(c, n, 4), [c.rows(m) for m in n], [c.rows(m) for m in n]
+        calls.append((n, q, k, v, c.attend(q, k, v)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    torch.cuda.synchronize()
+    args = []
+    for n, q, k, v, _ in calls:
+        qd, cu, total, most = c.ragged(q)
+        kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 4, total, most), dtype=torch.uint8, device="cuda")
+        o = torch.empty((total, 4 * c.dim), dtype=torch.float16, device="cuda")
+        ls = torch.empty((total, 4), device="cuda")
+        args.append((qd, qd.stride(0), 4, kd, vd, kd.stride(0), o, ls, cu, most, ws, False, total))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, a in zip(streams, args):
+            fq.flex_paged_attention(c.cache, *a[:11], accumulate=a[11], total=a[12], stream=st)
+    torch.cuda.synchronize()
+    sync_status()
+    for a, (_, _, _, _, (o, ls)) in zip(args, calls):
+        total = a[12]
+        assert torch.equal(a[6], o[:total]) and torch.equal(a[7], ls[:total])
+
+
+@pytest.mark.parametrize("bits,dim,group,page", [(4, 64, 32, 16), (4, 128, 64, 64), (8, 64, 64, 16), (8, 128, 32, 128)])
+@pytest.mark.parametrize("budget,recent", [(1, 0), (1, 1), (16, 3), (40, 40), (64, 0), (100, 20)])
+def test_evict(bits, dim, group, page, budget, recent):
+    ctx = [0, 1, 63, 64, 65, 200, 101]
+    c = Case(15, ctx, heads=3, dim=dim, bits=bits, group=group, page=page)
+    _evict(c, budget, recent)
+
+
+def _evict(c, budget, recent, fill=True):
+    if fill:
+        w = c.r.standard_normal(tuple(c.cache.weight.shape)).astype(np.float32)
+        w[c.r.random(w.shape) < 0.4] = 0.25                # many equal ones
+        w[c.r.random(w.shape) < 0.05] = np.nan
+        w[c.r.random(w.shape) < 0.05] = np.inf
+        w[c.r.random(w.shape) < 0.05] = -0.0
+        w[c.r.random(w.shape) < 0.05] = -np.inf
+        c.cache.weight.copy_(torch.from_numpy(w))
+        c.ref.weight = w.astype(np.float64)
+        pos = c.r.permutation(w.size).astype(np.int32).reshape(w.shape)
+        c.cache.slot_pos.copy_(torch.from_numpy(pos))
+        c.ref.pos = pos.copy()
+    new = torch.zeros(c.cache.batch, dtype=torch.int32, device="cuda")
+    ws = torch.full((fq.flex_paged_evict_ws_bytes(c.cache, budget),), 0xFF, dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(c.cache, budget, recent, new, ws)
+    sync_status()
+    lens = c.ref.evict(budget, recent)
+    assert np.array_equal(to_np(new), lens)
+    c.set_ctx(lens)
+    c.check_slots("evicted")
+    for b, n in enumerate(lens):
+        if n:
+            ref = np.stack([c.ref.weight[c.ref.at(b, j)[0], :, c.ref.at(b, j)[1]] for j in range(int(n))], 1)
+            assert np.array_equal(c.slots(c.cache.weight, b, int(n)).astype(np.float64), ref, equal_nan=True), b
+
+
+def test_evict_many_slots():
+    """More slots than the selection keeps in shared memory at once."""
+    n = 40000
+    c = Case(16, [0, 0], heads=2, dim=64, bits=4, group=64, page=1024, room=n)
+    w = torch.rand(tuple(c.cache.weight.shape), device="cuda").mul_(64).round_()
+    pos = torch.randperm(w.numel(), device="cuda").to(torch.int32).view(w.shape)
+    for t in (c.cache.k_codes, c.cache.v_codes):
+        t.random_(0, 256)
+    c.cache.weight.copy_(w)
+    c.cache.slot_pos.copy_(pos)
+    c.ctx.copy_(torch.tensor([n, 33000], dtype=torch.int32))
+    codes = c.cache.k_codes.clone()
+    budget, recent = 9000, 500
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fq.flex_paged_evict_ws_bytes(c.cache, budget), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(c.cache, budget, recent, new, ws)
+    sync_status()
+    assert new.tolist() == [budget, budget]
+    for b, m in enumerate((n, 33000)):
+        ids = to_np(c.cache.page_table[b]).astype(np.int64)
+        for h in range(2):
+            ww, pp = (to_np(t[ids, h]).reshape(-1)[:m] for t in (w, pos))
+            first = pp > pp.max() - recent
+            order = np.lexsort((np.arange(m), -np.where(first, 0, ww), ~first))
+            kept = np.zeros(m, bool)
+            kept[order[:budget]] = True
+            src = np.arange(budget)
+            src[~kept[:budget]] = np.nonzero(kept)[0][kept[:budget].sum():]
+            got = to_np(c.cache.slot_pos[ids, h]).reshape(-1)[:budget]
+            assert np.array_equal(got, pp[src])
+            old, now = (to_np(t[ids, h]).reshape(-1, codes.shape[-1])[:m] for t in (codes, c.cache.k_codes))
+            assert np.array_equal(now[:budget], old[src]) and np.array_equal(now[budget:], old[budget:])
+
+
+def test_a_bounded_cache_step_by_step():
+    """Chunks, single tokens and evictions in turn, as a serving loop uses the operators; the
+    oracle follows with the device's own weights, so that equal choices are compared."""
+    c = Case(17, [0, 0, 0], heads=2, dim=64, bits=4, group=64, page=16, room=96)
+    pos = np.zeros(3, np.int64)
+    budget, recent = 48, 12
+    for n in ([40, 7, 1], [1, 30, 1], [20, 1, 33], [1, 1, 1], [1, 1, 1], [30, 2, 0], [1, 1, 1]):
+        q, k, v = _scaled(c, n, 4), [c.rows(m) for m in n], [c.rows(m) for m in n]
+        c.attend(q, k, v, accumulate=True)
+        c.store(k, v, advance=True, pos0=pos.astype(np.int32))
+        pos += n
+        c.check_slots("stored")
+        c.ref.weight = to_np(c.cache.weight).astype(np.float64)
+        _evict(c, budget, recent, fill=False)
+
+
+def test_captured_calls_follow_their_inputs():
+    """A captured step replayed with other lengths, tables and rows."""
+    c = Case(18, [700, 30, 0], heads=2, dim=64, room=64)
+    n0 = [1, 40, 9]
+    q, k, v = _scaled(c, n0, 4), [c.rows(m) for m in n0], [c.rows(m) for m in n0]
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    o = torch.empty((total, 4 * c.dim), dtype=torch.float16, device="cuda")
+    ls = torch.empty((total, 4), device="cuda")
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 4, total, most, True), dtype=torch.uint8, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(c.cache, 600), dtype=torch.uint8, device="cuda")
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+
+    def step():
+        fq.flex_paged_attention(c.cache, qd, qd.stride(0), 4, kd, vd, kd.stride(0), o, ls, cu, most, ws, accumulate=True,
+                                total=total)
+        fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), cu, most, total=total)
+        fq.flex_paged_evict(c.cache, 600, 50, new, ew)
+
+    weight, pools = c.cache.weight.clone(), [t.clone() for t in (c.cache.k_codes, c.cache.k_meta, c.cache.v_codes,
+                                                                  c.cache.v_meta, c.cache.slot_pos)]
+
+    def restore():
+        for t, x in zip((c.cache.k_codes, c.cache.k_meta, c.cache.v_codes, c.cache.v_meta, c.cache.slot_pos), pools):
+            t.copy_(x)
+        c.cache.weight.copy_(weight)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()                                             # kernels are loaded outside the capture
+    torch.cuda.synchronize()
+    restore()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, ctx in ((n0, [700, 30, 0]), ([40, 1, 9], [650, 30, 0]), ([0, 0, 50 - 12], [700, 30, 0])):
+        restore()
+        cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32))
+        c.set_ctx(ctx)
+        graph.replay()
+        sync_status()
+        qh, kh, vh = (to_np(x[:, :w]) for x, w in ((qd, 4 * c.dim), (kd, 2 * c.dim), (vd, 2 * c.dim)))
+        ends = np.concatenate([[0], np.cumsum(n)])
+        parts = [[x[a:b].reshape(b - a, x.shape[1] // c.dim, c.dim) for a, b in zip(ends[:-1], ends[1:])] for x in (qh, kh, vh)]
+        m = int(ends[-1])
+        c.check_attention(*parts, torch.cat([o[:m]]), ls[:m])
+        assert new.tolist() == [min(x, 600) for x in ctx]
+
+
+def test_two_captured_steps_with_their_own_workspaces():
+    c = Case(19, [2500, 900], heads=1, dim=64, page=64, room=2)
+    graphs = []
+    for n in ([1, 1], [2, 1]):
+        q, k, v = _scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n]
+        want = c.attend(q, k, v)
+        qd, cu, total, most = c.ragged(q)
+        kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 2, total, most), dtype=torch.uint8, device="cuda")
+        o = torch.empty((total, 2 * c.dim), dtype=torch.float16, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fq.flex_paged_attention(c.cache, qd, qd.stride(0), 2, kd, vd, kd.stride(0), o, None, cu, most, ws, total=total)
+        graphs.append((g, o, want[0][:total], (qd, kd, vd, cu, ws)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, (g, _, _, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    sync_status()
+    for _, o, want, _ in graphs:
+        assert torch.equal(o, want)
+
+
+def _status():
+    rc = fq.flex_get_status()
+    assert fq.flex_get_status() == fq.FLEX_OK              # it is cleared
+    return rc
+
+
+def test_bad_pages_and_lengths_are_reported():
+    """Page ids outside the pool, lengths outside the table and offsets that do not fit are
+    reported; nothing is touched through them and the other sequences are right."""
+    c = Case(20, [40, 30, 25], heads=2, dim=64, room=16)
+    n = [1, 2, 1]
+    q, k, v = _scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    good, _ = c.attend(q, k, v)
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 2, total, most, True), dtype=torch.uint8, device="cuda")
+    o = torch.empty((total, 2 * c.dim), dtype=torch.float16, device="cuda")
+    table, ctx, offs = c.cache.page_table.clone(), c.ctx.clone(), cu.clone()
+
+    def attend(acc=False):
+        fq.flex_paged_attention(c.cache, qd, qd.stride(0), 2, kd, vd, kd.stride(0), o, None, cu, most, ws, total=total,
+                                accumulate=acc)
+        return _status()
+
+    def bad(what, where, value, rows):
+        what[where] = value
+        for acc in (False, True):
+            assert attend(acc) == fq.FLEX_ERR_INVALID_ARG
+            assert all(torch.equal(o[r], good[r]) for r in rows)
+        c.cache.page_table.copy_(table)
+        c.ctx.copy_(ctx)
+        cu.copy_(offs)
+
+    bad(c.cache.page_table, (1, 0), c.cache.num_pages, [0, 3])
+    bad(c.cache.page_table, (1, 1), -1, [0, 3])
+    bad(c.ctx, 0, -5, [1, 2, 3])
+    bad(c.ctx, 2, 1 << 29, [0, 1, 2])
+    bad(cu, 2, 0, [0])                                     # decreasing
+    bad(cu, 3, total + 7, [0, 1, 2])                       # behind the rows
+    bad(cu, 1, -3, [3])
+    before = [t.clone() for t in (c.cache.k_codes, c.cache.v_meta, c.cache.slot_pos)]
+    c.ctx[1] = table.shape[1] * c.page                     # no slot left in the table
+    fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), cu, most, total=total)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG
+    p0 = int(table[1, -1])
+    if p0 >= 0:
+        assert torch.equal(c.cache.k_codes[p0], before[0][p0])
+    c.ctx.copy_(ctx)
+    out = torch.full((total, 2 * c.dim), 5.0, dtype=torch.float16, device="cuda")
+    for start in (-1, 1 << 29):
+        s = torch.tensor([0, start, 0], dtype=torch.int32, device="cuda")
+        fq.flex_paged_load_kv(c.cache, out, out.clone(), 2 * c.dim, cu, most, total=total, start=s)
+        assert _status() == fq.FLEX_ERR_INVALID_ARG
+        assert bool((out[1] == 5).all()) and not bool((out[0] == 5).all())
+    c.cache.page_table[0, 0] = 1 << 30
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(c.cache, 8), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(c.cache, 8, 2, new, ew)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG and new.tolist() == [8, 8, 8]
+
+
+def test_overlapping_offsets_are_survived():
+    """Offsets that repeat rows ask for more tiles than `total` allows: reported or not, no
+    call reads or writes outside its tensors, and the next call is right."""
+    c = Case(21, [3000] * 6, heads=1, dim=64, page=64, room=2)
+    n = [1] * 6
+    q, k, v = _scaled(c, n, 1), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    good, _ = c.attend(q, k, v)
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    ws = torch.full((fq.flex_paged_attention_ws_bytes(c.cache, 1, total, 6),), 0x7F, dtype=torch.uint8, device="cuda")
+    o = torch.empty((total, c.dim), dtype=torch.float16, device="cuda")
+    cu.copy_(torch.tensor([0, 6, 0, 6, 0, 6, 0], dtype=torch.int32))
+    fq.flex_paged_attention(c.cache, qd, qd.stride(0), 1, kd, vd, kd.stride(0), o, None, cu, 6, ws, total=total)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG
+    again, _ = c.attend(q, k, v)
+    assert torch.equal(good, again)
+
+
+def test_pool_larger_than_32_bit_offsets():
+    """Slots whose byte offsets pass 2^32, at the end of the pool."""
+    pages, heads, page, dim = 1 << 13, 40, 128, 128        # 41.9 M slots of 128 bytes: 5.4 GB a pool
+    table = torch.tensor([[pages - 1, pages - 3], [pages - 2, 0]], dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    shape = (pages, heads, page)
+    pools = tuple(torch.empty(shape + s, dtype=t, device="cuda") for s, t in
+                  (((dim,), torch.uint8), ((2, 2), torch.float16)) * 2)
+    cache = fq.FlexPagedCache(table, ctx, pools=pools, weight=True, slot_pos=True, num_bits=8, group_size=64)
+    assert cache.k_codes.numel() > 1 << 32
+    r = np.random.default_rng(22)
+    rows = [r.standard_normal((140, heads, dim)).astype(np.float16) for _ in range(4)]
+    ref = PagedCache([[0, 1], [2, 3]], [0, 0], 4, page, heads, dim, 8, 64)
+    kd, vd = (torch.from_numpy(np.concatenate(x).reshape(280, -1)).cuda() for x in (rows[:2], rows[2:]))
+    fq.flex_paged_store_kv(cache, kd, vd, heads * dim, None, 140)
+    for b in range(2):
+        ref.store(b, rows[b], rows[2 + b])
+    out = [torch.empty_like(kd), torch.empty_like(vd)]
+    fq.flex_paged_load_kv(cache, *out, heads * dim, None, 140)
+    ctx.fill_(140)
+    ref.ctx[:] = 140
+    sync_status()
+    for b in range(2):
+        for x, want in zip(out, ref.load(b, 0, 140)):
+            assert np.array_equal(to_np(x[b * 140:b * 140 + 140]).reshape(140, heads, dim), want)
+    for n in (1, 33):
+        q = (r.standard_normal((2 * n, heads, dim)) * 0.09).astype(np.float16)
+        o = torch.empty((2 * n, heads * dim), dtype=torch.float16, device="cuda")
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(cache, heads, 2 * n, n, True), dtype=torch.uint8, device="cuda")
+        fq.flex_paged_attention(cache, torch.from_numpy(q).cuda().view(2 * n, -1), heads * dim, heads, None, None, 0, o, None,
+                                None, n, ws, accumulate=True)
+        sync_status()
+        for b in range(2):
+            small = PagedCache([[0, 1], [2, 3]], [140, 140], 4, page, 1, dim, 8, 64)
+            for h in (0, heads - 1):
+                for name in "kv":
+                    small.codes[name][:, 0], small.meta[name][:, 0] = ref.codes[name][:, h], ref.meta[name][:, h]
+                want = small.attend(b, q[b * n:b * n + n, h:h + 1])[0][:, 0]
+                got = to_np(o[b * n:b * n + n, h * dim:(h + 1) * dim]).astype(np.float64)
+                assert np.all(np.abs(got - want) <= U * np.abs(want) + 2 * U * 5.0)
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(cache, 100), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(cache, 100, 10, new, ew)
+    sync_status()
+    assert new.tolist() == [100, 100]
+
+
+def test_the_whole_batch_is_empty():
+    c = Case(23, [0, 0], heads=2, room=16)
+    c.attend([c.rows(0, 2), c.rows(0, 2)], [c.rows(0), c.rows(0)], [c.rows(0), c.rows(0)])
+    o, ls = c.attend(_scaled(c, [2, 1], 2))
+    assert not bool(o[:3].any()) and bool((ls[:3] == float("-inf")).all())
