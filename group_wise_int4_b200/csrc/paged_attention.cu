@@ -7,194 +7,12 @@
 // base 2 (scores times log2 e), probabilities are rounded to fp16 once, as operands of the
 // value product: at most 2^-11 of each, far below o's own fp16 rounding after the sum.
 // k_j and v_j are the fp16 values of paged.cuh, so the products are exact and summed in fp32.
-#include <float.h>
-
 #include <type_traits>
 
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace flexq {
 namespace {
-
-__device__ __forceinline__ void cp16(uint32_t s, const void* g, bool ok) {
-    const int n = ok ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_small(uint32_t s, const void* g, bool ok) {
-    const int n = ok ? N : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(s), "l"(g), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands
-__device__ __forceinline__ void mma168(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t mat_trans(uint32_t x) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-// ---- operands -------------------------------------------------------------------------
-//
-// Scores are S^T = K Q^T: keys are the rows of the 16 x 8 products, query rows the columns.
-// Lane (g, t) of a quad row takes the dims [t D/4, (t+1) D/4) of its keys, so a key's codes
-// are one contiguous piece per lane; the product does not care which dims a k-step holds
-// as long as both operands agree. At 4 bits the nibble pairs of a word are (d, d+4),
-// (d+1, d+5), ..., at 8 bits the byte pairs are neighbours; the query is laid out to match.
-
-// Query operand of row g of an 8-row tile: D/16 k-steps of two registers.
-template <int D, int BITS>
-__device__ __forceinline__ void load_query(uint32_t (&bq)[D / 16][2], const __half* row, int t, bool ok) {
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {                 // 8 dims: two k-steps
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (ok) x = __ldg(reinterpret_cast<const uint4*>(row + t * (D / 4)) + u);
-        if (BITS == 4) {
-            bq[2 * u][0] = byte_perm(x.x, x.z, 0x5410u);
-            bq[2 * u][1] = byte_perm(x.x, x.z, 0x7632u);
-            bq[2 * u + 1][0] = byte_perm(x.y, x.w, 0x5410u);
-            bq[2 * u + 1][1] = byte_perm(x.y, x.w, 0x7632u);
-        } else {
-            bq[2 * u][0] = x.x;
-            bq[2 * u][1] = x.y;
-            bq[2 * u + 1][0] = x.z;
-            bq[2 * u + 1][1] = x.w;
-        }
-    }
-}
-
-// Key operand of two k-steps (8 dims) from 8 codes: at 4 bits one word, at 8 bits two.
-template <int BITS>
-__device__ __forceinline__ void key_pairs(uint32_t (&a)[4], uint32_t w0, uint32_t w1, uint32_t step, uint32_t mn) {
-    if (BITS == 4) {
-        const uint32_t y = w0 >> 8;
-        a[0] = h2_fma(codes_lo(w0), step, mn);
-        a[1] = h2_fma(codes_hi(w0), step, mn);
-        a[2] = h2_fma(codes_lo(y), step, mn);
-        a[3] = h2_fma(codes_hi(y), step, mn);
-    } else {
-        a[0] = h2_fma(codes_b01(w0), step, mn);
-        a[1] = h2_fma(codes_b23(w0), step, mn);
-        a[2] = h2_fma(codes_b01(w1), step, mn);
-        a[3] = h2_fma(codes_b23(w1), step, mn);
-    }
-}
-// The same from 8 fresh fp16 values.
-template <int BITS>
-__device__ __forceinline__ void key_pairs_fresh(uint32_t (&a)[4], uint4 x) {
-    if (BITS == 4) {
-        a[0] = byte_perm(x.x, x.z, 0x5410u);
-        a[1] = byte_perm(x.x, x.z, 0x7632u);
-        a[2] = byte_perm(x.y, x.w, 0x5410u);
-        a[3] = byte_perm(x.y, x.w, 0x7632u);
-    } else {
-        a[0] = x.x;
-        a[1] = x.y;
-        a[2] = x.z;
-        a[3] = x.w;
-    }
-}
-
-// Pairs of fp16 values: does one have the largest exponent (infinity or NaN), and the same
-// with those taken for 0.
-__device__ __forceinline__ uint32_t wild_halves(uint32_t x) { return __vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
-__device__ __forceinline__ bool any_wild(uint4 x) {
-    return (wild_halves(x.x) | wild_halves(x.y) | wild_halves(x.z) | wild_halves(x.w)) != 0u;
-}
-__device__ __forceinline__ uint4 without_wild(uint4 x) {
-    return make_uint4(x.x & ~wild_halves(x.x), x.y & ~wild_halves(x.y), x.z & ~wild_halves(x.z), x.w & ~wild_halves(x.w));
-}
-
-// ---- work split -------------------------------------------------------------------------
-//
-// A unit is (sequence, tile of R query rows, part of the key length); one block per unit
-// and key head. The key length of all sequences together is cut into parts of `part`
-// blocks of KEYS keys, so that about `target` blocks share it whatever its distribution:
-// every warp finds its block's unit by itself from ctx_len and cu (a few loads and
-// shuffles), so nothing has to be planned on the host or in another launch.
-struct RowsPlan {
-    int batch, share, target, heads;
-};
-
-struct Unit {
-    int b, tile, part, parts, per;      // per: key blocks in a part
-    int first, n, ctx;
-    bool live;
-};
-
-template <int R, int KEYS>
-__device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
-    const int lane = threadIdx.x & 31;
-    // work of the whole batch, in key blocks times row tiles
-    int64_t work = 0;
-    for (int b = lane; b < p.batch; b += 32) {
-        int first;
-        const int n = rows_of(rows, b, first, c.status);
-        const int64_t tiles = (static_cast<int64_t>(n) * p.share + R - 1) / R;
-        work += tiles * ((slots_of(c, b) + KEYS - 1) / KEYS);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
-    // at least two blocks of keys a part: less costs more to join than it saves
-    const int64_t even = (work * p.heads + p.target - 1) / p.target;
-    Unit u{};
-    u.per = static_cast<int>(even < 2 ? 2 : even > (1 << 30) ? (1 << 30) : even);
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        int n = 0, ctx = 0, first = 0, tiles = 0, parts = 0;
-        if (b < p.batch) {
-            n = rows_of(rows, b, first, c.status);
-            ctx = slots_of(c, b);
-            tiles = static_cast<int>((static_cast<int64_t>(n) * p.share + R - 1) / R);
-            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.per - 1) / u.per);
-        }
-        const int64_t mine = static_cast<int64_t>(tiles) * parts;
-        int64_t x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        x += before;                                    // units up to and with b
-        const unsigned has = __ballot_sync(0xffffffffu, unit < x);
-        if (has) {
-            const int l = __ffs(has) - 1;
-            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, x - mine, l));
-            u.b = b0 + l;
-            u.n = __shfl_sync(0xffffffffu, n, l);
-            u.ctx = __shfl_sync(0xffffffffu, ctx, l);
-            u.first = __shfl_sync(0xffffffffu, first, l);
-            u.parts = __shfl_sync(0xffffffffu, parts, l);
-            u.tile = at / u.parts;
-            u.part = at % u.parts;
-            u.live = true;
-            return u;
-        }
-        before = __shfl_sync(0xffffffffu, x, 31);
-    }
-    return u;
-}
-
-// Where a row tile's parts are: written by its part 0 for the joining kernel.
-struct TileRecord {
-    int parts, slot;      // parts lie at partial slots [slot, slot + parts)
-};
 
 // ---- few rows: one warp's 16 keys against 8 or 16 query rows ------------------------------
 //
@@ -223,13 +41,11 @@ __device__ __forceinline__ int value_piece(int key, int c) {
 }
 
 template <int D, int BITS, int GS, int NR>
-__global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf rows, RowsPlan plan,
-                                                         const __half* __restrict__ q, int64_t q_stride,
-                                                         const __half* __restrict__ k_new,
-                                                         const __half* __restrict__ v_new, int64_t kv_stride,
-                                                         __half* __restrict__ o, float* __restrict__ lse,
-                                                         float* __restrict__ parts_ws, TileRecord* __restrict__ records,
-                                                         int most_tiles) {
+__global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
+    const PagedView& c = A.c;
+    const RowsPlan& plan = A.plan;
+    const __half *k_new = A.k_new, *v_new = A.v_new;
+    const int64_t kv_stride = A.kv_stride;
     using S = RowsShape<D, BITS>;
     constexpr int KB = S::KB, KW = S::KW, KEYS = S::KEYS, ST = S::STAGES;
     constexpr int NG = D / GS, R = 8 * NR, KT = KW / 16;
@@ -239,7 +55,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf row
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.x % plan.heads, unit = blockIdx.x / plan.heads;
-    const Unit u = find_unit<R, KEYS>(c, rows, plan, unit);
+    const Unit u = find_unit<R, KEYS, 2>(c, A.rows, plan, unit);
     if (!u.live) return;
     const int blocks = (u.ctx + KEYS - 1) / KEYS;
     const int key0 = min(blocks, u.part * u.per) * KEYS;
@@ -291,7 +107,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf row
         const int r = row0 + n * 8 + g;
         const bool ok = r < row_end;
         const int i = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
-        load_query<D, BITS>(bq[n], q + static_cast<int64_t>(u.first + i) * q_stride + h * D, t, ok);
+        load_query<D, BITS>(bq[n], A.q + static_cast<int64_t>(u.first + i) * A.q_stride + h * D, t, ok);
 #pragma unroll
         for (int e = 0; e < 2; ++e) token[n][e] = (row0 + n * 8 + 2 * t + e) / plan.share;
     }
@@ -575,13 +391,8 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf row
             for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][n][e], acc[i][n][2 + e]);
         }
     __syncthreads();
-    const int tile_id = u.b * most_tiles + u.tile;
-    if (tid == 0 && u.part == 0 && u.parts > 1) {
-        // partial slots of (sequence, tile, part) lie side by side: the tile's first is this block's
-        records[static_cast<int64_t>(tile_id) * plan.heads + head] = TileRecord{u.parts, unit};
-    } else if (tid == 0 && u.part == 0) {
-        records[static_cast<int64_t>(tile_id) * plan.heads + head] = TileRecord{1, 0};
-    }
+    if (tid == 0 && u.part == 0)
+        A.records[static_cast<int64_t>(u.b * A.most_tiles + u.tile) * plan.heads + head] = TileRecord{u.parts, u.slot};
     for (int i = tid; i < R * (D / 4); i += 128) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         if (row0 + r >= row_end) continue;
@@ -604,11 +415,10 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf row
             const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
             const int64_t at = static_cast<int64_t>(u.first + tok) * (plan.heads * plan.share) + h;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2*>(o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-            if (d == 0 && lse) lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        } else {
-            // [unit][head][row][D + 4]: the output, then maximum and sum
-            float* p = parts_ws + ((static_cast<int64_t>(unit) * plan.heads + head) * R + r) * (D + 4);
+            *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+            if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        } else if (u.slot < A.slots) {
+            float* p = A.parts + ((static_cast<int64_t>(u.slot) * plan.heads + head) * R + r) * (D + 4);
             *reinterpret_cast<float4*>(p + d) = a;
             if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(top, sum);
         }
@@ -616,25 +426,24 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(PagedView c, RowsOf row
 }
 
 // Joins the parts of one row tile (of R rows) and key head.
-template <int D, int R>
-__global__ void __launch_bounds__(128) paged_join_kernel(PagedView c, RowsOf rows, RowsPlan plan, const float* __restrict__ parts_ws,
-                                                         const TileRecord* __restrict__ records, __half* __restrict__ o,
-                                                         float* __restrict__ lse, int most_tiles, int units) {
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A, int R) {
     pdl_wait();
     pdl_trigger();
+    const RowsPlan& plan = A.plan;
     const int head = blockIdx.x % plan.heads, tile_id = blockIdx.x / plan.heads;
-    const int b = tile_id / most_tiles, row0 = (tile_id % most_tiles) * R;
+    const int b = tile_id / A.most_tiles, row0 = (tile_id % A.most_tiles) * R;
     int first;
-    const int row_end = rows_of(rows, b, first, c.status) * plan.share;
+    const int row_end = rows_of(A.rows, b, first, A.c.status) * plan.share;
     if (row0 >= row_end) return;
-    const TileRecord rec = records[static_cast<int64_t>(tile_id) * plan.heads + head];
+    const TileRecord rec = A.records[static_cast<int64_t>(tile_id) * plan.heads + head];
     // offsets that overlap (cu out of order) can leave a tile without a unit, its record unset
-    if (rec.parts <= 1 || rec.slot < 0 || rec.parts > units || rec.slot > units - rec.parts) return;
+    if (rec.parts <= 1 || rec.slot < 0 || rec.parts > A.slots || rec.slot > A.slots - rec.parts) return;
     for (int i = threadIdx.x; i < R * (D / 4); i += 128) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         if (row0 + r >= row_end) break;
         const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
-        const float* p = parts_ws + ((static_cast<int64_t>(rec.slot) * plan.heads + head) * R + r) * (D + 4);
+        const float* p = A.parts + ((static_cast<int64_t>(rec.slot) * plan.heads + head) * R + r) * (D + 4);
         float top = -FLT_MAX;
         for (int k = 0; k < rec.parts; ++k) top = fmaxf(top, __ldg(p + k * step + D));
         float sum = 0.f;
@@ -652,8 +461,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(PagedView c, RowsOf row
         const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
         const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-        if (d == 0 && lse) lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+        if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -664,9 +473,12 @@ __global__ void __launch_bounds__(128) paged_join_kernel(PagedView c, RowsOf row
 // rows of the sequence, so every key's sum stays in its lanes and is added in one fixed
 // order; no atomics. Query rows pass through shared memory, 32 at a time, for 4 warps.
 template <int D, int BITS, int GS>
-__global__ void __launch_bounds__(128) paged_weight_kernel(PagedView c, RowsOf rows, RowsPlan plan, const __half* __restrict__ q,
-                                                           int64_t q_stride, const __half* __restrict__ k_new, int64_t kv_stride,
-                                                           const float* __restrict__ lse) {
+__global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
+    const PagedView& c = A.c;
+    const RowsPlan& plan = A.plan;
+    const __half *q = A.q, *k_new = A.k_new;
+    const int64_t q_stride = A.q_stride, kv_stride = A.kv_stride;
+    const float* lse = A.lse;
     constexpr int KB = D * BITS / 8, NG = D / GS, QR = 32, LD = D + 8;
     __shared__ __align__(16) __half sq[2][QR * LD];
     __shared__ float sl[2][QR];
@@ -675,7 +487,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(PagedView c, RowsOf r
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
-    const int n = rows_of(rows, b, first, c.status), ctx = slots_of(c, b), cap = paged_capacity(c);
+    const int n = rows_of(A.rows, b, first, c.status), ctx = slots_of(c, b), cap = paged_capacity(c);
     const int old_blocks = (ctx + 127) / 128;
     const bool fresh = static_cast<int>(blockIdx.x) >= old_blocks;
     const int j0 = (static_cast<int>(blockIdx.x) - (fresh ? old_blocks : 0)) * 128 + warp * 32;    // slot, or fresh token
@@ -795,7 +607,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(PagedView c, RowsOf r
 // ---- host -----------------------------------------------------------------------------------
 
 struct AttnPlan {
-    int share, row_tile, most_tiles, target;
+    int share, row_tile, most_tiles, target, slots;
     int64_t units, records_bytes, parts_bytes, lse_bytes;
     int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes; }
 };
@@ -805,15 +617,17 @@ inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total, int most, bool accumulate) {
     AttnPlan p{};
     p.share = n_heads / c->n_kv_heads;
-    p.row_tile = static_cast<int64_t>(most) * p.share <= 8 ? 8 : 16;
-    p.most_tiles = static_cast<int>((static_cast<int64_t>(most) * p.share + p.row_tile - 1) / p.row_tile);
+    const int64_t rows = static_cast<int64_t>(most) * p.share;
+    p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
+    p.most_tiles = static_cast<int>((rows + p.row_tile - 1) / p.row_tile);
     // blocks wanted on the device at once: 4 a multiprocessor
-    p.target = 4 * sm_count();
-    // every sequence's row tiles, and what their parts add: at most target blocks over all heads
-    const int64_t tiles = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch;
-    p.units = tiles + (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
+    p.target = p.row_tile <= 16 ? 4 * sm_count() : paged_tile_target(p.row_tile, c->head_dim);
+    // every sequence's row tiles, and what their parts add (the bounds stand at find_unit)
+    const int64_t more = (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
+    p.units = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch + more;
+    p.slots = static_cast<int>(2 * more);
     p.records_bytes = up256(static_cast<int64_t>(batch) * p.most_tiles * c->n_kv_heads * sizeof(TileRecord));
-    p.parts_bytes = up256(p.units * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
+    p.parts_bytes = up256(static_cast<int64_t>(p.slots) * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
     p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
     return p;
 }
@@ -866,51 +680,58 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     const int kvh = cache->n_kv_heads;
     FLEX_REQUIRE(p.units * kvh < (1LL << 31) && static_cast<int64_t>(batch) * p.most_tiles * kvh < (1LL << 31),
                  FLEX_ERR_UNSUPPORTED);
-    FLEX_REQUIRE(static_cast<int64_t>(most) * p.share < (1LL << 31), FLEX_ERR_UNSUPPORTED);
+    FLEX_REQUIRE(static_cast<int64_t>(most) * p.share < (1LL << 31) - 512, FLEX_ERR_UNSUPPORTED);
 
-    const PagedView view = paged_view(cache);
-    const RowsOf rows{cu_new, most, total};
-    const RowsPlan plan{batch, p.share, p.target, kvh};
-    const cudaStream_t st = as_stream(stream);
+    AttnArgs a{};
+    a.c = paged_view(cache);
+    a.rows = RowsOf{cu_new, most, total};
+    a.plan = RowsPlan{batch, p.share, p.target, kvh};
+    a.q = static_cast<const __half*>(q);
+    a.q_stride = q_stride;
+    a.k_new = static_cast<const __half*>(k_new);
+    a.v_new = static_cast<const __half*>(v_new);
+    a.kv_stride = kv_stride;
+    a.o = static_cast<__half*>(o);
     unsigned char* w = static_cast<unsigned char*>(ws);
-    TileRecord* records = reinterpret_cast<TileRecord*>(w);
-    float* parts = reinterpret_cast<float*>(w + p.records_bytes);
-    if (lse == nullptr && accumulate) lse = reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes);
-    const __half* qh = static_cast<const __half*>(q);
-    const __half* kn = static_cast<const __half*>(k_new);
-    const __half* vn = static_cast<const __half*>(v_new);
-    __half* oh = static_cast<__half*>(o);
+    a.records = reinterpret_cast<TileRecord*>(w);
+    a.parts = reinterpret_cast<float*>(w + p.records_bytes);
+    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes) : lse;
+    a.most_tiles = p.most_tiles;
+    a.slots = p.slots;
+    const cudaStream_t st = as_stream(stream);
     const dim3 grid(static_cast<unsigned>(p.units * kvh)), join(static_cast<unsigned>(static_cast<int64_t>(batch) * p.most_tiles * kvh));
     const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;
+    if (p.row_tile > 16) {
+        launch_paged_tile(a, D, B, G, p.row_tile, p.units, st);
+    } else {
 #define ROWS(D_, B_, G_, N_)                                                                                        \
     do {                                                                                                            \
         constexpr int ring = RowsShape<D_, B_>::STAGES * 4 * RowsShape<D_, B_>::KW * 2 * (RowsShape<D_, B_>::KB + D_ / G_ * 4); \
         constexpr int outs = 4 * 8 * N_ * D_ * 4, smem = ring > outs ? ring : outs;                                 \
         set_smem_once(paged_rows_kernel<D_, B_, G_, N_>, smem);                                                     \
-        launch_k(paged_rows_kernel<D_, B_, G_, N_>, grid, dim3(128), smem, st, true, view, rows, plan, qh, q_stride, kn, vn, \
-                 kv_stride, oh, lse, parts, records, p.most_tiles);                                                 \
-        launch_k(paged_join_kernel<D_, 8 * N_>, join, dim3(128), 0, st, true, view, rows, plan,                     \
-                 static_cast<const float*>(parts), static_cast<const TileRecord*>(records), oh, lse, p.most_tiles, \
-                 static_cast<int>(p.units));                                                                        \
+        launch_k(paged_rows_kernel<D_, B_, G_, N_>, grid, dim3(128), smem, st, true, a);                            \
     } while (0)
 #define ROWS_N(D_, B_, G_) \
     do { if (p.row_tile == 8) ROWS(D_, B_, G_, 1); else ROWS(D_, B_, G_, 2); } while (0)
-    if (D == 64) {
-        if (B == 4 && G == 32) ROWS_N(64, 4, 32); else if (B == 4) ROWS_N(64, 4, 64);
-        else if (G == 32) ROWS_N(64, 8, 32); else ROWS_N(64, 8, 64);
-    } else {
-        if (B == 4 && G == 32) ROWS_N(128, 4, 32); else if (B == 4) ROWS_N(128, 4, 64);
-        else if (G == 32) ROWS_N(128, 8, 32); else ROWS_N(128, 8, 64);
-    }
+        if (D == 64) {
+            if (B == 4 && G == 32) ROWS_N(64, 4, 32); else if (B == 4) ROWS_N(64, 4, 64);
+            else if (G == 32) ROWS_N(64, 8, 32); else ROWS_N(64, 8, 64);
+        } else {
+            if (B == 4 && G == 32) ROWS_N(128, 4, 32); else if (B == 4) ROWS_N(128, 4, 64);
+            else if (G == 32) ROWS_N(128, 8, 32); else ROWS_N(128, 8, 64);
+        }
 #undef ROWS_N
 #undef ROWS
+    }
+    if (D == 64)
+        launch_k(paged_join_kernel<64>, join, dim3(128), 0, st, true, a, p.row_tile);
+    else
+        launch_k(paged_join_kernel<128>, join, dim3(128), 0, st, true, a, p.row_tile);
     if (accumulate) {
         const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
         // every 128 slots, and 128 fresh tokens; blocks behind a sequence's end return at once
         const dim3 wgrid(static_cast<unsigned>((cap + 127) / 128 + (k_new ? (most + 127) / 128 : 0)), kvh, batch);
-#define WEIGHT(D_, B_, G_)                                                                                       \
-    launch_k(paged_weight_kernel<D_, B_, G_>, wgrid, dim3(128), 0, st, true, view, rows, plan, qh, q_stride, kn, kv_stride, \
-             static_cast<const float*>(lse))
+#define WEIGHT(D_, B_, G_) launch_k(paged_weight_kernel<D_, B_, G_>, wgrid, dim3(128), 0, st, true, a)
         if (D == 64) {
             if (B == 4 && G == 32) WEIGHT(64, 4, 32); else if (B == 4) WEIGHT(64, 4, 64);
             else if (G == 32) WEIGHT(64, 8, 32); else WEIGHT(64, 8, 64);

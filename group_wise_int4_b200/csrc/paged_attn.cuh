@@ -1,0 +1,227 @@
+// What the attention kernels over a paged cache share: operands from codes, the split of
+// the work and its plan.
+#pragma once
+
+#include <float.h>
+
+#include "paged.cuh"
+
+namespace flexq {
+
+__device__ __forceinline__ void cp16(uint32_t s, const void* g, bool ok) {
+    const int n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t s, const void* g, bool ok) {
+    const int n = ok ? N : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(s), "l"(g), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands
+__device__ __forceinline__ void mma168(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mat_trans(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// ---- operands -------------------------------------------------------------------------
+//
+// Scores are S^T = K Q^T: keys are the rows of the 16 x 8 products, query rows the columns.
+// Lane (g, t) of a quad row takes the dims [t D/4, (t+1) D/4) of its keys, so a key's codes
+// are one contiguous piece per lane; the product does not care which dims a k-step holds
+// as long as both operands agree. At 4 bits the nibble pairs of a word are (d, d+4),
+// (d+1, d+5), ..., at 8 bits the byte pairs are neighbours; the query is laid out to match.
+
+// Query operand of row g of an 8-row tile: D/16 k-steps of two registers.
+template <int D, int BITS>
+__device__ __forceinline__ void load_query(uint32_t (&bq)[D / 16][2], const __half* row, int t, bool ok) {
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {                 // 8 dims: two k-steps
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (ok) x = __ldg(reinterpret_cast<const uint4*>(row + t * (D / 4)) + u);
+        if (BITS == 4) {
+            bq[2 * u][0] = byte_perm(x.x, x.z, 0x5410u);
+            bq[2 * u][1] = byte_perm(x.x, x.z, 0x7632u);
+            bq[2 * u + 1][0] = byte_perm(x.y, x.w, 0x5410u);
+            bq[2 * u + 1][1] = byte_perm(x.y, x.w, 0x7632u);
+        } else {
+            bq[2 * u][0] = x.x;
+            bq[2 * u][1] = x.y;
+            bq[2 * u + 1][0] = x.z;
+            bq[2 * u + 1][1] = x.w;
+        }
+    }
+}
+
+// Key operand of two k-steps (8 dims) from 8 codes: at 4 bits one word, at 8 bits two.
+template <int BITS>
+__device__ __forceinline__ void key_pairs(uint32_t (&a)[4], uint32_t w0, uint32_t w1, uint32_t step, uint32_t mn) {
+    if (BITS == 4) {
+        const uint32_t y = w0 >> 8;
+        a[0] = h2_fma(codes_lo(w0), step, mn);
+        a[1] = h2_fma(codes_hi(w0), step, mn);
+        a[2] = h2_fma(codes_lo(y), step, mn);
+        a[3] = h2_fma(codes_hi(y), step, mn);
+    } else {
+        a[0] = h2_fma(codes_b01(w0), step, mn);
+        a[1] = h2_fma(codes_b23(w0), step, mn);
+        a[2] = h2_fma(codes_b01(w1), step, mn);
+        a[3] = h2_fma(codes_b23(w1), step, mn);
+    }
+}
+// The same from 8 fresh fp16 values.
+template <int BITS>
+__device__ __forceinline__ void key_pairs_fresh(uint32_t (&a)[4], uint4 x) {
+    if (BITS == 4) {
+        a[0] = byte_perm(x.x, x.z, 0x5410u);
+        a[1] = byte_perm(x.x, x.z, 0x7632u);
+        a[2] = byte_perm(x.y, x.w, 0x5410u);
+        a[3] = byte_perm(x.y, x.w, 0x7632u);
+    } else {
+        a[0] = x.x;
+        a[1] = x.y;
+        a[2] = x.z;
+        a[3] = x.w;
+    }
+}
+
+// Pairs of fp16 values: does one have the largest exponent (infinity or NaN), and the same
+// with those taken for 0.
+__device__ __forceinline__ uint32_t wild_halves(uint32_t x) { return __vcmpeq2(x & 0x7C007C00u, 0x7C007C00u); }
+__device__ __forceinline__ bool any_wild(uint4 x) {
+    return (wild_halves(x.x) | wild_halves(x.y) | wild_halves(x.z) | wild_halves(x.w)) != 0u;
+}
+__device__ __forceinline__ uint4 without_wild(uint4 x) {
+    return make_uint4(x.x & ~wild_halves(x.x), x.y & ~wild_halves(x.y), x.z & ~wild_halves(x.z), x.w & ~wild_halves(x.w));
+}
+
+// ---- work split -------------------------------------------------------------------------
+//
+// A unit is (sequence, tile of R query rows, part of the key length); one block per unit
+// and key head. The key length of all sequences together is cut into parts of `per`
+// blocks of KEYS keys, so that about `target` blocks share it whatever its distribution:
+// every warp finds its block's unit by itself from ctx_len and cu (a few loads and
+// shuffles), so nothing has to be planned on the host or in another launch.
+//
+// Bounds that the workspace relies on, with work = sum of row tiles times key blocks and
+// per >= work * heads / target: tiles are at most total * share / R + batch; the parts
+// beyond each tile's first at most work / per <= target / heads; and the units of tiles
+// that are split (ceil(blocks / per) < 2 blocks / per, as blocks > per) fewer than
+// 2 target / heads: only those have a slot for partial results.
+struct RowsPlan {
+    int batch, share, target, heads;
+};
+
+struct Unit {
+    int b, tile, part, parts, per;      // per: key blocks in a part
+    int slot;                           // of this unit's partial result, where parts > 1
+    int first, n, ctx;
+    bool live;
+};
+
+// MIN: blocks of keys that a part has at least; less costs more to join than it saves.
+template <int R, int KEYS, int MIN>
+__device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
+    const int lane = threadIdx.x & 31;
+    // work of the whole batch, in key blocks times row tiles
+    int64_t work = 0;
+    for (int b = lane; b < p.batch; b += 32) {
+        int first;
+        const int n = rows_of(rows, b, first, c.status);
+        const int64_t tiles = (static_cast<int64_t>(n) * p.share + R - 1) / R;
+        work += tiles * ((slots_of(c, b) + KEYS - 1) / KEYS);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    const int64_t even = (work * p.heads + p.target - 1) / p.target;
+    Unit u{};
+    u.per = static_cast<int>(even < MIN ? MIN : even > (1 << 30) ? (1 << 30) : even);
+    int64_t before = 0, split = 0;                      // units, and units of split tiles, of the sequences passed
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int n = 0, ctx = 0, first = 0, tiles = 0, parts = 0;
+        if (b < p.batch) {
+            n = rows_of(rows, b, first, c.status);
+            ctx = slots_of(c, b);
+            tiles = static_cast<int>((static_cast<int64_t>(n) * p.share + R - 1) / R);
+            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.per - 1) / u.per);
+        }
+        const int64_t mine = static_cast<int64_t>(tiles) * parts, mine2 = parts > 1 ? mine : 0;
+        int64_t x = mine, y = mine2;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t xx = __shfl_up_sync(0xffffffffu, x, o), yy = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) {
+                x += xx;
+                y += yy;
+            }
+        }
+        x += before;                                    // up to and with b
+        y += split;
+        const unsigned has = __ballot_sync(0xffffffffu, unit < x);
+        if (has) {
+            const int l = __ffs(has) - 1;
+            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, x - mine, l));
+            u.b = b0 + l;
+            u.n = __shfl_sync(0xffffffffu, n, l);
+            u.ctx = __shfl_sync(0xffffffffu, ctx, l);
+            u.first = __shfl_sync(0xffffffffu, first, l);
+            u.parts = __shfl_sync(0xffffffffu, parts, l);
+            u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
+            u.slot = static_cast<int>(__shfl_sync(0xffffffffu, y - mine2, l)) + at;
+            u.tile = at / u.parts;
+            u.part = at % u.parts;
+            u.live = true;
+            return u;
+        }
+        before = __shfl_sync(0xffffffffu, x, 31);
+        split = __shfl_sync(0xffffffffu, y, 31);
+    }
+    return u;
+}
+
+// Where a row tile's parts are: written by its part 0 for the joining kernel.
+struct TileRecord {
+    int parts, slot;      // parts lie at partial slots [slot, slot + parts)
+};
+
+// What a launch of either attention kernel gets. Partial results: [slot][head][row of the
+// tile][D + 4]: the output, then the maximum (base 2) and the sum.
+struct AttnArgs {
+    PagedView c;
+    RowsOf rows;
+    RowsPlan plan;
+    const __half* q;
+    int64_t q_stride;
+    const __half *k_new, *v_new;
+    int64_t kv_stride;
+    __half* o;
+    float* lse;
+    float* parts;
+    TileRecord* records;
+    int most_tiles, slots;      // row tiles of the longest sequence; partial slots
+};
+
+// The tcgen05 kernel over tiles of paged_tile_rows() query rows; `units` blocks per key head.
+int paged_tile_rows(int rows);
+int paged_tile_target(int row_tile, int head_dim);
+void launch_paged_tile(const AttnArgs& a, int head_dim, int bits, int group, int row_tile, int64_t units, cudaStream_t st);
+
+}  // namespace flexq
