@@ -31,6 +31,8 @@ struct RowsShape {
     static constexpr int STAGES = 3;
 };
 
+constexpr int kRowsMin = 2;        // blocks of keys that a part has at least
+
 // 16-byte piece i of a warp's KW keys, in keys' order, is put where the value product reads
 // without bank conflicts: lanes (g, t) read piece(s) g of keys 2t, 2t + 1, ....
 template <int KB>
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.x % plan.heads, unit = blockIdx.x / plan.heads;
-    const Unit u = find_unit<R, KEYS, 2>(c, A.rows, plan, unit);
+    const Unit u = find_unit<R, KEYS, kRowsMin>(c, A.rows, plan, unit);
     if (!u.live) return;
     const int blocks = (u.ctx + KEYS - 1) / KEYS;
     const int key0 = min(blocks, u.part * u.per) * KEYS;
@@ -391,8 +393,6 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
             for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][n][e], acc[i][n][2 + e]);
         }
     __syncthreads();
-    if (tid == 0 && u.part == 0)
-        A.records[static_cast<int64_t>(u.b * A.most_tiles + u.tile) * plan.heads + head] = TileRecord{u.parts, u.slot};
     for (int i = tid; i < R * (D / 4); i += 128) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         if (row0 + r >= row_end) continue;
@@ -422,47 +422,6 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
             *reinterpret_cast<float4*>(p + d) = a;
             if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(top, sum);
         }
-    }
-}
-
-// Joins the parts of one row tile (of R rows) and key head.
-template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A, int R) {
-    pdl_wait();
-    pdl_trigger();
-    const RowsPlan& plan = A.plan;
-    const int head = blockIdx.x % plan.heads, tile_id = blockIdx.x / plan.heads;
-    const int b = tile_id / A.most_tiles, row0 = (tile_id % A.most_tiles) * R;
-    int first;
-    const int row_end = rows_of(A.rows, b, first, A.c.status) * plan.share;
-    if (row0 >= row_end) return;
-    const TileRecord rec = A.records[static_cast<int64_t>(tile_id) * plan.heads + head];
-    // offsets that overlap (cu out of order) can leave a tile without a unit, its record unset
-    if (rec.parts <= 1 || rec.slot < 0 || rec.parts > A.slots || rec.slot > A.slots - rec.parts) return;
-    for (int i = threadIdx.x; i < R * (D / 4); i += 128) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        if (row0 + r >= row_end) break;
-        const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
-        const float* p = A.parts + ((static_cast<int64_t>(rec.slot) * plan.heads + head) * R + r) * (D + 4);
-        float top = -FLT_MAX;
-        for (int k = 0; k < rec.parts; ++k) top = fmaxf(top, __ldg(p + k * step + D));
-        float sum = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < rec.parts; ++k) {
-            const float2 ml = __ldg(reinterpret_cast<const float2*>(p + k * step + D));
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + k * step + d));
-            const float f = exp2_fast(ml.x - top);
-            sum = fmaf(f, ml.y, sum);
-            a.x = fmaf(f, x.x, a.x);
-            a.y = fmaf(f, x.y, a.y);
-            a.z = fmaf(f, x.z, a.z);
-            a.w = fmaf(f, x.w, a.w);
-        }
-        const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
-        const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-        if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -607,9 +566,9 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
 // ---- host -----------------------------------------------------------------------------------
 
 struct AttnPlan {
-    int share, row_tile, most_tiles, target, slots;
-    int64_t units, records_bytes, parts_bytes, lse_bytes;
-    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes; }
+    int share, row_tile, target, slots;
+    int64_t units, parts_bytes, lse_bytes;
+    int64_t bytes() const { return parts_bytes + lse_bytes; }
 };
 
 inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -619,14 +578,12 @@ AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total,
     p.share = n_heads / c->n_kv_heads;
     const int64_t rows = static_cast<int64_t>(most) * p.share;
     p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
-    p.most_tiles = static_cast<int>((rows + p.row_tile - 1) / p.row_tile);
     // blocks wanted on the device at once: 4 a multiprocessor
     p.target = p.row_tile <= 16 ? 4 * sm_count() : paged_tile_target(p.row_tile, c->head_dim);
     // every sequence's row tiles, and what their parts add (the bounds stand at find_unit)
     const int64_t more = (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
     p.units = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch + more;
     p.slots = static_cast<int>(2 * more);
-    p.records_bytes = up256(static_cast<int64_t>(batch) * p.most_tiles * c->n_kv_heads * sizeof(TileRecord));
     p.parts_bytes = up256(static_cast<int64_t>(p.slots) * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
     p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
     return p;
@@ -678,8 +635,7 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     FLEX_REQUIRE(aligned16(ws), FLEX_ERR_ALIGN);
     if (most == 0 || total == 0) return FLEX_OK;
     const int kvh = cache->n_kv_heads;
-    FLEX_REQUIRE(p.units * kvh < (1LL << 31) && static_cast<int64_t>(batch) * p.most_tiles * kvh < (1LL << 31),
-                 FLEX_ERR_UNSUPPORTED);
+    FLEX_REQUIRE(p.units * kvh < (1LL << 31), FLEX_ERR_UNSUPPORTED);
     FLEX_REQUIRE(static_cast<int64_t>(most) * p.share < (1LL << 31) - 512, FLEX_ERR_UNSUPPORTED);
 
     AttnArgs a{};
@@ -693,13 +649,11 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     a.kv_stride = kv_stride;
     a.o = static_cast<__half*>(o);
     unsigned char* w = static_cast<unsigned char*>(ws);
-    a.records = reinterpret_cast<TileRecord*>(w);
-    a.parts = reinterpret_cast<float*>(w + p.records_bytes);
-    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes) : lse;
-    a.most_tiles = p.most_tiles;
+    a.parts = reinterpret_cast<float*>(w);
+    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.parts_bytes) : lse;
     a.slots = p.slots;
     const cudaStream_t st = as_stream(stream);
-    const dim3 grid(static_cast<unsigned>(p.units * kvh)), join(static_cast<unsigned>(static_cast<int64_t>(batch) * p.most_tiles * kvh));
+    const dim3 grid(static_cast<unsigned>(p.units * kvh));
     const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;
     if (p.row_tile > 16) {
         launch_paged_tile(a, D, B, G, p.row_tile, p.units, st);
@@ -710,6 +664,7 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
         constexpr int outs = 4 * 8 * N_ * D_ * 4, smem = ring > outs ? ring : outs;                                 \
         set_smem_once(paged_rows_kernel<D_, B_, G_, N_>, smem);                                                     \
         launch_k(paged_rows_kernel<D_, B_, G_, N_>, grid, dim3(128), smem, st, true, a);                            \
+        launch_join<D_, 8 * N_, RowsShape<D_, B_>::KEYS, kRowsMin>(a, st);                                          \
     } while (0)
 #define ROWS_N(D_, B_, G_) \
     do { if (p.row_tile == 8) ROWS(D_, B_, G_, 1); else ROWS(D_, B_, G_, 2); } while (0)
@@ -723,10 +678,6 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
 #undef ROWS_N
 #undef ROWS
     }
-    if (D == 64)
-        launch_k(paged_join_kernel<64>, join, dim3(128), 0, st, true, a, p.row_tile);
-    else
-        launch_k(paged_join_kernel<128>, join, dim3(128), 0, st, true, a, p.row_tile);
     if (accumulate) {
         const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
         // every 128 slots, and 128 fresh tokens; blocks behind a sequence's end return at once

@@ -137,7 +137,8 @@ struct Unit {
 };
 
 // MIN: blocks of keys that a part has at least; less costs more to join than it saves.
-template <int R, int KEYS, int MIN>
+// SPLIT: `unit` counts the units of split tiles alone (it is a partial slot).
+template <int R, int KEYS, int MIN, bool SPLIT = false>
 __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
     const int lane = threadIdx.x & 31;
     // work of the whole batch, in key blocks times row tiles
@@ -175,10 +176,10 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
         }
         x += before;                                    // up to and with b
         y += split;
-        const unsigned has = __ballot_sync(0xffffffffu, unit < x);
+        const unsigned has = __ballot_sync(0xffffffffu, unit < (SPLIT ? y : x));
         if (has) {
             const int l = __ffs(has) - 1;
-            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, x - mine, l));
+            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, SPLIT ? y - mine2 : x - mine, l));
             u.b = b0 + l;
             u.n = __shfl_sync(0xffffffffu, n, l);
             u.ctx = __shfl_sync(0xffffffffu, ctx, l);
@@ -197,11 +198,6 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
     return u;
 }
 
-// Where a row tile's parts are: written by its part 0 for the joining kernel.
-struct TileRecord {
-    int parts, slot;      // parts lie at partial slots [slot, slot + parts)
-};
-
 // What a launch of either attention kernel gets. Partial results: [slot][head][row of the
 // tile][D + 4]: the output, then the maximum (base 2) and the sum.
 struct AttnArgs {
@@ -215,9 +211,58 @@ struct AttnArgs {
     __half* o;
     float* lse;
     float* parts;
-    TileRecord* records;
-    int most_tiles, slots;      // row tiles of the longest sequence; partial slots
+    int slots;                  // of partial results
 };
+
+// Joins the parts of split tiles. Block (slot, head, z): the rows of the slot's tile are
+// shared out evenly over its parts' slots and z, so that every block reads about as much.
+template <int D, int R, int KEYS, int MIN>
+__global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
+    pdl_wait();
+    pdl_trigger();
+    const RowsPlan& plan = A.plan;
+    const int head = blockIdx.x % plan.heads;
+    const Unit u = find_unit<R, KEYS, MIN, true>(A.c, A.rows, plan, blockIdx.x / plan.heads);
+    if (!u.live || u.slot - u.part + u.parts > A.slots) return;
+    const int row0 = u.tile * R, rows = min(R, u.n * plan.share - row0);
+    const int chunks = u.parts * gridDim.y, chunk = u.part * gridDim.y + blockIdx.y, per = (rows + chunks - 1) / chunks;
+    constexpr int L = D / 4;                            // lanes of a row
+    const int d = (threadIdx.x % L) * 4;
+    const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
+    for (int r = chunk * per + threadIdx.x / L; r < min(rows, (chunk + 1) * per); r += 128 / L) {
+        const float* p = A.parts + ((static_cast<int64_t>(u.slot - u.part) * plan.heads + head) * R + r) * (D + 4);
+        float top = -FLT_MAX;
+#pragma unroll 8
+        for (int k = 0; k < u.parts; ++k) top = fmaxf(top, __ldg(p + k * step + D));
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < u.parts; ++k) {
+            const float2 ml = __ldg(reinterpret_cast<const float2*>(p + k * step + D));
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + k * step + d));
+            const float f = exp2_fast(ml.x - top);
+            sum = fmaf(f, ml.y, sum);
+            a.x = fmaf(f, x.x, a.x);
+            a.y = fmaf(f, x.y, a.y);
+            a.z = fmaf(f, x.z, a.z);
+            a.w = fmaf(f, x.w, a.w);
+        }
+        const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
+        const int64_t at = static_cast<int64_t>(u.first + tok) * (plan.heads * plan.share) + h;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+        if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+}
+
+// A part has at least MIN blocks of keys, so a table of no more splits nothing and needs no
+// joining launch.
+template <int D, int R, int KEYS, int MIN>
+void launch_join(const AttnArgs& a, cudaStream_t st) {
+    if (static_cast<int64_t>(a.c.max_pages) << a.c.shift <= static_cast<int64_t>(MIN) * KEYS) return;
+    launch_k(paged_join_kernel<D, R, KEYS, MIN>, dim3(static_cast<unsigned>(a.slots * a.plan.heads), R <= 16 ? 1 : R / 32),
+             dim3(128), 0, st, true, a);
+}
 
 // The tcgen05 kernel over tiles of paged_tile_rows() query rows; `units` blocks per key head.
 int paged_tile_rows(int rows);

@@ -2,18 +2,23 @@
 // accumulators in tensor memory (tcgen05).
 //
 // A block holds TILES tiles of 128 query rows (tokens of a sequence times the heads that
-// share a key head) and walks over its keys, 128 at a time. The keys' codes become fp16
-// operands once per block of keys and serve all of the block's rows: at 256 rows that is
-// about 1.9 K warp instructions beside 2048 cycles of matrix products, so dequantising in
-// the kernel costs less than writing the fp16 values to memory and reading them again.
+// share a key head) and walks over its keys, 64 at a time. The keys' codes become fp16
+// operands once per block of keys and serve all of the block's rows.
 //
 //   dequant warps   codes -> registers (a block of keys ahead) -> fp16 K and V in shared
-//                   memory, one key a thread: its steps and minima are worked out once
-//   matrix warp     S_t = Q_t K^T (both from shared memory), O_t += P_t V (P_t from tensor
+//                   memory; a thread takes a key or a value and works out its steps once
+//   matrix warps    S_t = Q_t K^T (both from shared memory), O_t += P_t V (P_t from tensor
 //                   memory, over S_t's columns; V as an MN-major operand, so K and V
 //                   have the same layout and neither is transposed)
-//   softmax warps   one row a thread: maximum, exp2, sum, P_t; with two tiles the products
-//                   of one run while the exponentials of the other are taken
+//   softmax warps   one row a thread: maximum, exp2, sum, P_t
+//
+// S_t has two buffers, so that the products of one block of keys run while the
+// exponentials of the one before are taken, and the next S is there when they are done.
+// That is why blocks have 64 keys: at head_dim 128 two tiles take 2 (2 * 64 + 128) = 512
+// columns, all there are. With 128 keys and one buffer each step waited for the other
+// (wait, S, softmax, P V in turn): 5100 cycles per 128 keys and 256 rows. One warp that
+// issues all products: 1745 us for 2000 tokens over 8 to 16 thousand slots at 32 heads of
+// 128, one a tile 1169, one for each kind and tile 1018.
 //
 // The running maximum m only moves when a score passes it by more than 2^8 (in base 2, 8
 // steps): until then the probabilities are up to 256 instead of 1, which fp16 holds with
@@ -26,13 +31,18 @@
 namespace flexq {
 namespace {
 
+constexpr int kTileMin = 4;        // blocks of keys that a part has at least
+
+constexpr int NK = 64;             // keys of a block
+
 template <int D, int TILES>
 struct TileShape {
-    static constexpr int ST = (TILES == 1 && D == 128) ? 1 : 2;    // stages of K and of V: two blocks an SM at 1 tile
-    static constexpr int BLOCK = 128 * D * 2;                      // bytes of 128 fp16 rows
-    static constexpr int SMEM = (TILES + 2 * ST) * BLOCK + 1024;
-    static constexpr int COLS = TILES == 1 ? 256 : 512;            // tensor memory: TILES * (128 + D) columns
-    static constexpr int THREADS = TILES * 128 + 128 + 32;
+    static constexpr int ST = TILES == 1 && D == 128 ? 2 : 4;      // stages of K and of V: two blocks an SM at 1 tile
+    static constexpr int QB = 128 * D * 2, BLOCK = NK * D * 2;     // bytes of a tile's queries, of a block of keys
+    static constexpr int SMEM = TILES * QB + 2 * ST * BLOCK + 1024;
+    static constexpr int COLS = TILES == 1 ? 256 : 512;            // tensor memory: TILES * (2 * NK + D) columns
+    static constexpr int SOFT = TILES * 4;                         // softmax warps, then 4 dequant warps and the matrix warp
+    static constexpr int THREADS = SOFT * 32 + 128 + 64 * TILES;
 };
 
 __device__ __forceinline__ void sts16(uint32_t at, const uint32_t (&a)[4]) {
@@ -64,20 +74,21 @@ __device__ __forceinline__ uint64_t f32x2_scale(uint64_t a, float f) {
     return r;
 }
 
-// 16-byte piece c (8 dims) of row r of an operand: halves of 64 dims, rows of 128 bytes,
-// the hardware's 128-byte swizzle. 8 threads that write one piece of consecutive rows hit
+// 16-byte piece c (8 dims) of row r of an operand: blocks of 64 dims (ROWS rows each), rows
+// of 128 bytes, the hardware's 128-byte swizzle. 8 threads that write one piece of consecutive rows hit
 // 8 different bank groups.
+template <int ROWS>
 __device__ __forceinline__ uint32_t piece_at(uint32_t base, int r, int c) {
-    return base + (c >> 3) * 16384 + r * 128 + ((c & 7) ^ (r & 7)) * 16;
+    return base + (c >> 3) * (ROWS * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16;
 }
 
 template <int D, int BITS, int GS, int TILES>
 __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 : 1)
     paged_tile_kernel(AttnArgs A, uint64_t wait_ns) {
     using T = TileShape<D, TILES>;
-    constexpr int ST = T::ST, KB = D * BITS / 8, NG = D / GS, R = TILES * 128, NX = KB / 16;
+    constexpr int ST = T::ST, KB = D * BITS / 8, NG = D / GS, R = TILES * 128, NX = KB / 16, SOFT = T::SOFT;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t bars[4 * ST + 1 + 3 * TILES + 1];
+    __shared__ __align__(8) uint64_t bars[4 * ST + 1 + 8 * TILES];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, wild_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -85,54 +96,66 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     pdl_wait();
     pdl_trigger();
     const int head = blockIdx.x % A.plan.heads;
-    const Unit u = find_unit<R, 128, 4>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
+    const Unit u = find_unit<R, 128, kTileMin>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
     if (!u.live) return;
     const int share = A.plan.share;
     const int blocks = (u.ctx + 127) / 128;
     const int key0 = min(blocks, u.part * u.per) * 128;
     const int key1 = min(u.ctx, min(blocks, (u.part + 1) * u.per) * 128);
-    const int nc = (key1 - key0 + 127) / 128;                 // blocks of cached keys
+    const int nc = (key1 - key0 + NK - 1) / NK;               // blocks of cached keys
     const int row_end = u.n * share, row0 = u.tile * R;
     // fresh tokens that any of the rows sees, by the last part
     const int last = A.k_new != nullptr && u.part == u.parts - 1 ? (min(row_end, row0 + R) - 1) / share + 1 : 0;
-    const int nb = nc + (last + 127) / 128;
+    const int nb = nc + (last + NK - 1) / NK;
     const int tiles = min(TILES, (row_end - row0 + 127) / 128);
 
     const uint32_t bar0 = tc::smem_u32(bars);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
-                   q_full = v_empty + 8 * ST, s_full = q_full + 8, p_full = s_full + 8 * TILES, o_done = p_full + 8 * TILES,
-                   drain = o_done + 8 * TILES;
-    const uint32_t sq = (tc::smem_u32(raw) + 1023u) & ~1023u, sk = sq + TILES * T::BLOCK, sv = sk + ST * T::BLOCK;
+                   q_full = v_empty + 8 * ST, s_full = q_full + 8, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
+                   drain = o_done + 16 * TILES;
+    const uint32_t sq = (tc::smem_u32(raw) + 1023u) & ~1023u, sk = sq + TILES * T::QB, sv = sk + ST * T::BLOCK;
     volatile int* abort = &abort_flag;
     int* const status = c.status;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            tc::bar_init(k_full + 8 * i, 128);
-            tc::bar_init(k_empty + 8 * i, 1);
-            tc::bar_init(v_full + 8 * i, 128);
-            tc::bar_init(v_empty + 8 * i, 1);
+            tc::bar_init(k_full + 8 * i, 2);          // one arrival a warp
+            tc::bar_init(k_empty + 8 * i, tiles);
+            tc::bar_init(v_full + 8 * i, 2);
+            tc::bar_init(v_empty + 8 * i, tiles);
         }
-        tc::bar_init(q_full, 128 * tiles);
+        tc::bar_init(q_full, 4 * tiles);
         for (int t = 0; t < TILES; ++t) {
-            tc::bar_init(s_full + 8 * t, 1);
-            tc::bar_init(p_full + 8 * t, 128);
-            tc::bar_init(o_done + 8 * t, 1);
+            // one for each S buffer: softmax may be a block ahead of the products, and they of it
+            for (int i = 0; i < 2; ++i) {
+                tc::bar_init(s_full + 16 * t + 8 * i, 1);
+                tc::bar_init(p_full + 16 * t + 8 * i, 4);
+                tc::bar_init(o_done + 16 * t + 8 * i, 1);
+            }
         }
-        tc::bar_init(drain, 1);
+        for (int i = 0; i < 2 * TILES; ++i) tc::bar_init(drain + 8 * i, 1);
         tc::bar_fence_init();
         abort_flag = 0;
         wild_flag = 0;
     }
-    if (warp == TILES * 4 + 4) {
+    if (warp == SOFT + 4) {
         tc::tmem_alloc(tc::smem_u32(&tmem_slot), T::COLS);
         tc::tmem_relinquish();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
-    if (warp < TILES * 4) {
+    // a warp's threads wait and arrive as one: an abort leaves no part of it behind
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, abort, status, wait_ns)) != 0;
+    };
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar);
+    };
+
+    if (warp < SOFT) {
         // ---- softmax: one row a thread
         const int tile = warp >> 2, r = tid & 127, row = row0 + tile * 128 + r;
         const bool live = row < row_end;
@@ -148,93 +171,84 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             for (int i = 0; i < D / 8; ++i) {
                 uint32_t a[4];
                 key_pairs_fresh<BITS>(a, live ? __ldg(qr + i) : make_uint4(0, 0, 0, 0));
-                sts16(piece_at(sq + tile * T::BLOCK, r, i), a);
+                sts16(piece_at<128>(sq + tile * T::QB, r, i), a);
             }
             tc::fence_proxy_async_smem();
-            tc::bar_arrive(q_full);
+            arrive(q_full);
             for (int j = 0; j < nb; ++j) {
-                if (!tc::bar_wait(s_full + 8 * tile, j & 1, abort, status, wait_ns)) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = wait(s_full + 16 * tile + 8 * (j & 1), (j >> 1) & 1))) break;
                 tc::fence_after_sync();
                 // keys of the block that this row sees: the first `lim`
-                const int lim = j < nc ? key1 - key0 - j * 128 : token + 1 - (j - nc) * 128;
+                const int lim = j < nc ? key1 - key0 - j * NK : token + 1 - (j - nc) * NK;
+                const uint32_t tj = ts + (j & 1) * NK;
                 uint32_t x[2][32];
-                auto load = [&](int half) {
-                    tc::tmem_ld32(ts + half * 64, x[0]);
-                    tc::tmem_ld32(ts + half * 64 + 32, x[1]);
-                    tc::tmem_wait_ld(x[0]);
-                    tc::tmem_wait_ld(x[1]);
-                };
+                tc::tmem_ld32(tj, x[0]);
+                tc::tmem_ld32(tj + 32, x[1]);
+                tc::tmem_wait_ld(x[0]);
+                tc::tmem_wait_ld(x[1]);
                 auto block = [&](auto whole_c) {
                     constexpr bool WHOLE = decltype(whole_c)::value;
-                    auto score = [&](int half, int i) {
+                    auto score = [&](int i) {
                         const float v = __uint_as_float(x[i >> 5][i & 31]);
-                        return WHOLE || half * 64 + i < lim ? v : -INFINITY;
+                        return WHOLE || i < lim ? v : -INFINITY;
                     };
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int half = 1; half >= 0; --half) {      // the first half stays in registers
-                        load(half);
-#pragma unroll
-                        for (int i = 0; i < 64; i += 2)
-                            tops[(i >> 1) & 3] = fmaxf(fmaxf(tops[(i >> 1) & 3], score(half, i)), score(half, i + 1));
-                    }
+                    for (int i = 0; i < NK; i += 2)
+                        tops[(i >> 1) & 3] = fmaxf(fmaxf(tops[(i >> 1) & 3], score(i)), score(i + 1));
                     const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * kLog2e;
                     if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                        // O may be changed: S_j was issued after P_(j-1) V was done
                         const bool moves = top > m + 8.f;       // a row's result depends on no other row
                         const float f = moves ? exp2_fast(m - top) : 1.f;
                         m = moves ? top : m;
                         l = f32x2_scale(l, f);
                         if (j > 0) {
+                            if (!(ok = wait(o_done + 16 * tile + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1))) return;
+                            tc::fence_after_sync();
 #pragma unroll 1
-                            for (int i = 0; i < D; i += 32) {
-                                uint32_t y[32];
-                                tc::tmem_ld32(to + i, y);
-                                tc::tmem_wait_ld(y);
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t y[16];
+                                tc::tmem_ld16(to + i, y);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-                                tc::tmem_st32(to + i, y);
+                                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                                tc::tmem_st16(to + i, y);
                             }
-                            load(0);
                         }
                     }
                     const uint64_t scale = f32x2(kLog2e, kLog2e), shift = f32x2(-m, -m);
                     uint64_t sums[2] = {l, 0};
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        if (half == 1) load(1);
-                        uint32_t p[32];
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) {
+                        for (int i = 0; i < 32; i += 2) {
                             float y0, y1;
-                            f32x2_get(f32x2_fma(f32x2(score(half, i), score(half, i + 1)), scale, shift), y0, y1);
+                            f32x2_get(f32x2_fma(f32x2(score(half * 32 + i), score(half * 32 + i + 1)), scale, shift), y0, y1);
                             const float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
                             sums[(i >> 1) & 1] = f32x2_add(sums[(i >> 1) & 1], f32x2(p0, p1));
                             const __half2 hp = __floats2half2_rn(p0, p1);
                             p[i >> 1] = *reinterpret_cast<const uint32_t*>(&hp);
                         }
-                        tc::tmem_st32(ts + half * 32, p);
+                        tc::tmem_st16(tj + half * 16, p);
                     }
                     l = f32x2_add(sums[0], sums[1]);
                 };
-                if (__all_sync(0xffffffffu, lim >= 128))
+                if (__all_sync(0xffffffffu, lim >= NK))
                     block(std::true_type{});
                 else
                     block(std::false_type{});
+                if (!ok) break;
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
-                tc::bar_arrive(p_full + 8 * tile);
+                arrive(p_full + 16 * tile + 8 * (j & 1));
             }
-            if (ok && nb > 0) ok = tc::bar_wait(o_done + 8 * tile, (nb - 1) & 1, abort, status, wait_ns);
+            if (ok && nb > 0) ok = wait(o_done + 16 * tile + 8 * ((nb - 1) & 1), ((nb - 1) >> 1) & 1);
             tc::fence_after_sync();
         }
-        if (tile < tiles && __all_sync(0xffffffffu, ok)) {
-            float l0, sum;
-            f32x2_get(l, l0, sum);
-            sum += l0;
+        float l0, sum;
+        f32x2_get(l, l0, sum);
+        sum += l0;
+        if (ok) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t at = static_cast<int64_t>(u.first + token) * (A.plan.heads * share) + h;
             float* part = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + tile * 128 + r) * (D + 4);
@@ -291,19 +305,21 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     A.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                 }
             }
-            if (r == 0 && tile == 0 && u.part == 0)
-                A.records[static_cast<int64_t>(u.b * A.most_tiles + u.tile) * A.plan.heads + head] = TileRecord{u.parts, u.slot};
         }
-    } else if (warp < TILES * 4 + 4) {
-        // ---- codes to operands: one key a thread
-        const int key = tid - TILES * 128;
+    } else if (warp < SOFT + 4) {
+        // ---- codes to operands: two warps take the keys, two the values, one key a thread
+        const int key = tid & (NK - 1);
+        const bool second = warp >= SOFT + 2;
+        const uint8_t* codes = second ? c.vc : c.kc;
+        const uint32_t* metas = second ? c.vm : c.km;
+        const uint32_t dst = second ? sv : sk, full = second ? v_full : k_full, empty = second ? v_empty : k_empty;
         auto row_index = [&](int j) {
-            const int k = key0 + j * 128 + key;
+            const int k = key0 + j * NK + key;
             if (j >= nc || k >= key1) return -1;
             const int p = page_of(c, u.b, k);
             return p < 0 ? -1 : slot_row(c, p, head, k);
         };
-        auto load = [&](uint4 (&x)[NX], uint32_t (&meta)[NG], const uint8_t* codes, const uint32_t* metas, int row) {
+        auto load = [&](uint4 (&x)[NX], uint32_t (&meta)[NG], int row) {
             const uint4* src = reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row < 0 ? 0 : row) * KB);
 #pragma unroll
             for (int i = 0; i < NX; ++i) x[i] = row < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + i);
@@ -311,7 +327,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             for (int i = 0; i < NG; ++i) meta[i] = row < 0 ? 0u : __ldg(metas + static_cast<int64_t>(row) * NG + i);
         };
         // absent keys have minimum and step 0: their values are 0
-        auto convert = [&](const uint4 (&x)[NX], const uint32_t (&meta)[NG], uint32_t dst) {
+        auto convert = [&](const uint4 (&x)[NX], const uint32_t (&meta)[NG], uint32_t at) {
             uint32_t step[NG], mn[NG];
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
@@ -329,114 +345,109 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     key_pairs<BITS>(a, word(i), 0u, step[i * 8 / GS], mn[i * 8 / GS]);
                 else
                     key_pairs<BITS>(a, word(2 * i % (NX * 4)), word((2 * i + 1) % (NX * 4)), step[i * 8 / GS], mn[i * 8 / GS]);
-                sts16(piece_at(dst, key, i), a);
+                sts16(piece_at<NK>(at, key, i), a);
             }
         };
         bool ok = true;
-        auto slot_free = [&](uint32_t bar, int j) {
-            if (j < ST) return true;
-            return tc::bar_wait(bar + 8 * (j % ST), ((j / ST) - 1) & 1, abort, status, wait_ns);
+        auto slot_free = [&](int j) {
+            return j < ST || wait(empty + 8 * (j % ST), ((j / ST) - 1) & 1);
         };
-        auto publish = [&](uint32_t bar, int j) {
+        auto publish = [&](int j) {
             tc::fence_proxy_async_smem();
-            tc::bar_arrive(bar + 8 * (j % ST));
+            arrive(full + 8 * (j % ST));
         };
-        uint4 xk[NX], xv[NX];
-        uint32_t mk[NG], mv[NG];
-        int row = row_index(0);
-        load(xk, mk, c.kc, c.km, row);
-        for (int j = 0; j < nc && ok; ++j) {
-            load(xv, mv, c.vc, c.vm, row);
-            row = row_index(j + 1);
-            if (!(ok = slot_free(k_empty, j))) break;
-            convert(xk, mk, sk + (j % ST) * T::BLOCK);
-            publish(k_full, j);
-            load(xk, mk, c.kc, c.km, row);
-            if (!(ok = slot_free(v_empty, j))) break;
-            convert(xv, mv, sv + (j % ST) * T::BLOCK);
-            publish(v_full, j);
+        uint4 x[2][NX];
+        uint32_t meta[2][NG];
+        load(x[0], meta[0], row_index(0));
+        int row = row_index(1);
+        auto step = [&](int j, auto now_c) {
+            constexpr int NOW = decltype(now_c)::value;
+            load(x[1 - NOW], meta[1 - NOW], row);
+            row = row_index(j + 2);
+            if (!(ok = slot_free(j))) return;
+            convert(x[NOW], meta[NOW], dst + (j % ST) * T::BLOCK);
+            publish(j);
+        };
+        for (int j = 0; j < nc && ok; j += 2) {
+            step(j, std::integral_constant<int, 0>{});
+            if (j + 1 < nc && ok) step(j + 1, std::integral_constant<int, 1>{});
         }
         for (int j = nc; j < nb && ok; ++j) {
-            const int tok = (j - nc) * 128 + key;
+            const int tok = (j - nc) * NK + key;
             const bool there = tok < last;
-            const int64_t off = static_cast<int64_t>(u.first + (there ? tok : 0)) * A.kv_stride + head * D;
-            const uint4* xk4 = reinterpret_cast<const uint4*>(A.k_new + off);
-            const uint4* xv4 = reinterpret_cast<const uint4*>(A.v_new + off);
-            if (!(ok = slot_free(k_empty, j))) break;
+            const uint4* src = reinterpret_cast<const uint4*>((second ? A.v_new : A.k_new) +
+                                                              static_cast<int64_t>(u.first + (there ? tok : 0)) * A.kv_stride + head * D);
+            if (!(ok = slot_free(j))) break;
 #pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
-                uint32_t a[4];
-                key_pairs_fresh<BITS>(a, there ? __ldg(xk4 + i) : make_uint4(0, 0, 0, 0));
-                sts16(piece_at(sk + (j % ST) * T::BLOCK, key, i), a);
-            }
-            publish(k_full, j);
-            if (!(ok = slot_free(v_empty, j))) break;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                uint4 v = there ? __ldg(xv4 + i) : make_uint4(0, 0, 0, 0);
+                uint4 v = there ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                 // a hidden key's probability is 0, and 0 * infinity would be NaN
-                if (any_wild(v)) {
+                if (second && any_wild(v)) {
                     v = without_wild(v);
                     wild_flag = 1;
                 }
                 uint32_t a[4];
                 key_pairs_fresh<BITS>(a, v);
-                sts16(piece_at(sv + (j % ST) * T::BLOCK, key, i), a);
+                sts16(piece_at<NK>(dst + (j % ST) * T::BLOCK, key, i), a);
             }
-            publish(v_full, j);
+            publish(j);
         }
-    } else if (lane == 0) {
-        // ---- the matrix products
-        constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, 128), idesc_o = tc::idesc_f16_f32(128, D) | tc::kIdescBMnMajor;
-        auto scores = [&](int t, int j) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {                  // 16 dims a step: 32 bytes of a swizzled row
-                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                tc::mma_f16(tmem + t * 128, tc::desc_k_sw128(sq + t * T::BLOCK + off),
-                            tc::desc_k_sw128(sk + (j % ST) * T::BLOCK + off), idesc_s, k > 0);
-            }
-            tc::mma_commit(s_full + 8 * t);
+    } else if ((warp - SOFT - 4) / 2 < tiles) {
+        // ---- the matrix products, two warps a tile: the scores S_j, which take the columns of
+        // P_(j-2), and P_j V. Waiting for a barrier and committing cost 100 to 300 cycles each while
+        // the products load the shared memory; with a warp for each kind they hide behind products.
+        const int t = (warp - SOFT - 4) / 2;
+        const bool value = (warp - SOFT - 4) & 1;
+        const uint32_t leader = lane == 0, td = tmem + t * 128;
+        bool ok = true;
+        auto wait1 = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && wait(bar, parity);
+            return ok;
         };
-        bool ok = nb == 0 || tc::bar_wait(q_full, 0, abort, status, wait_ns);
-        if (ok && nb > 0) {
-            ok = tc::bar_wait(k_full, 0, abort, status, wait_ns);
-            if (ok) {
+        if (!value) {
+            constexpr uint32_t idesc = tc::idesc_f16_f32(128, NK);
+            // descriptors hold addresses in units of 16 bytes: offsets are added
+            const uint64_t a = tc::desc_k_sw128(sq + t * T::QB), dk = tc::desc_k_sw128(sk);
+            ok = nb == 0 || wait(q_full, 0);
+            for (int j = 0; j < nb && ok; ++j) {
+                const int s = j % ST, h = j & 1;
+                if (!wait1(k_full + 8 * s, (j / ST) & 1)) break;
+                if (j > 1 && !wait1(o_done + 16 * t + 8 * h, ((j - 2) >> 1) & 1)) break;
                 tc::fence_after_sync();
-                for (int t = 0; t < tiles; ++t) scores(t, 0);
-                if (nb > ST) tc::mma_commit(k_empty);
-            }
-        }
-        for (int j = 0; j < nb && ok; ++j) {
-            for (int t = 0; t < tiles && ok; ++t) {
-                if (t == 0) ok = tc::bar_wait(v_full + 8 * (j % ST), (j / ST) & 1, abort, status, wait_ns);
-                ok = ok && tc::bar_wait(p_full + 8 * t, j & 1, abort, status, wait_ns);
-                if (!ok) break;
-                tc::fence_after_sync();
+                const uint64_t b = dk + s * (T::BLOCK >> 4);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)                     // 16 keys a step
-                    tc::mma_f16_ts(tmem + TILES * 128 + t * D, tmem + t * 128 + k * 8,
-                                   tc::desc_mn_sw128(sv + (j % ST) * T::BLOCK + k * 2048, 16384), idesc_o, j > 0 || k > 0);
-                tc::mma_commit(o_done + 8 * t);
-                if (t == tiles - 1 && j + ST < nb) tc::mma_commit(v_empty + 8 * (j % ST));
-                if (j + 1 < nb) {
-                    if (t == 0) ok = tc::bar_wait(k_full + 8 * ((j + 1) % ST), ((j + 1) / ST) & 1, abort, status, wait_ns);
-                    // S takes the columns that P V reads
-                    ok = ok && tc::bar_wait(o_done + 8 * t, j & 1, abort, status, wait_ns);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    scores(t, j + 1);
-                    if (t == tiles - 1 && j + 1 + ST < nb) tc::mma_commit(k_empty + 8 * ((j + 1) % ST));
-                }
+                for (int k = 0; k < D / 16; ++k)                // 16 dims a step: 32 bytes of a swizzled row
+                    tc::mma_f16_if(leader, td + h * NK, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                                   b + (((k >> 2) * (NK * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
+                tc::mma_commit_if(leader, s_full + 16 * t + 8 * h);
+                if (j + ST < nb) tc::mma_commit_if(leader, k_empty + 8 * s);
+            }
+        } else {
+            constexpr uint32_t idesc = tc::idesc_f16_f32(128, D) | tc::kIdescBMnMajor;
+            const uint64_t dv = tc::desc_mn_sw128(sv, NK * 128);
+            for (int j = 0; j < nb && ok; ++j) {
+                const int s = j % ST, h = j & 1;
+                if (!wait1(v_full + 8 * s, (j / ST) & 1) || !wait1(p_full + 16 * t + 8 * h, (j >> 1) & 1)) break;
+                tc::fence_after_sync();
+                const uint64_t b = dv + s * (T::BLOCK >> 4);
+#pragma unroll
+                for (int k = 0; k < NK / 16; ++k)               // 16 keys a step
+                    tc::mma_f16_ts_if(leader, tmem + TILES * 128 + t * D, td + h * NK + k * 8, b + k * (2048 >> 4), idesc,
+                                      j > 0 || k > 0);
+                tc::mma_commit_if(leader, o_done + 16 * t + 8 * h);
+                if (j + ST < nb) tc::mma_commit_if(leader, v_empty + 8 * s);
             }
         }
         if (!ok) {                                              // what was issued reads shared memory: let it end
-            tc::mma_commit(drain);
-            tc::bar_wait(drain, 0, abort, status, wait_ns);
+            const uint32_t bar = drain + 8 * (warp - SOFT - 4);
+            tc::mma_commit_if(leader, bar);
+            wait(bar, 0);
         }
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == TILES * 4 + 4) {
+    if (warp == SOFT + 4) {
+        __syncwarp();
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, T::COLS);
     }
@@ -448,6 +459,7 @@ void launch_one(const AttnArgs& a, int64_t units, cudaStream_t st) {
     set_smem_once(paged_tile_kernel<D, BITS, GS, TILES>, T::SMEM);
     launch_k(paged_tile_kernel<D, BITS, GS, TILES>, dim3(static_cast<unsigned>(units * a.plan.heads)), dim3(T::THREADS),
              T::SMEM, st, true, a, pipeline_wait_ns());
+    launch_join<D, 128 * TILES, 128, kTileMin>(a, st);
 }
 
 }  // namespace
@@ -459,11 +471,7 @@ int paged_tile_rows(int rows) { return rows <= 128 ? 128 : 256; }
 int paged_tile_target(int row_tile, int) { return sm_count() * (row_tile == 128 ? 2 : 1) * 2; }
 
 void launch_paged_tile(const AttnArgs& a, int head_dim, int bits, int group, int row_tile, int64_t units, cudaStream_t st) {
-#define TILE(D_, B_, G_)                                                  \
-    do {                                                                  \
-        if (row_tile == 128) launch_one<D_, B_, G_, 1>(a, units, st);     \
-        else launch_one<D_, B_, G_, 2>(a, units, st);                     \
-    } while (0)
+#define TILE(D_, B_, G_) row_tile == 128 ? launch_one<D_, B_, G_, 1>(a, units, st) : launch_one<D_, B_, G_, 2>(a, units, st)
     if (head_dim == 64) {
         if (bits == 4 && group == 32) TILE(64, 4, 32); else if (bits == 4) TILE(64, 4, 64);
         else if (group == 32) TILE(64, 8, 32); else TILE(64, 8, 64);
