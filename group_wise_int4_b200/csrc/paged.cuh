@@ -74,6 +74,20 @@ __device__ __forceinline__ int page_of(const PagedView& c, int b, int s) {
     return p;
 }
 
+// The same in two steps, so that the table's entry is on its way while other work is done:
+// the entry itself (kNoPage where `there` is false), then its check and the row of slot s.
+constexpr int kNoPage = INT32_MIN;
+__device__ __forceinline__ int page_entry(const PagedView& c, const int32_t* table_row, int s, bool there) {
+    return there ? __ldg(table_row + (s >> c.shift)) : kNoPage;
+}
+__device__ __forceinline__ int entry_row(const PagedView& c, int entry, int head, int s) {
+    if (static_cast<unsigned>(entry) >= static_cast<unsigned>(c.num_pages)) {
+        if (entry != kNoPage) paged_bad(c);
+        return -1;
+    }
+    return ((entry * c.heads + head) << c.shift) + (s & ((1 << c.shift) - 1));
+}
+
 // Row index of slot s of a page (page >= 0) and head.
 __device__ __forceinline__ int slot_row(const PagedView& c, int page, int head, int s) {
     return ((page * c.heads + head) << c.shift) + (s & ((1 << c.shift) - 1));
@@ -109,8 +123,13 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
 }
 // Codes in the low nibbles of bits 0-3 and 16-19: with the exponent of 1024 behind them they
 // are 1024 + c; in bits 4-7 and 20-23, with that of 64, 64 + c. Both differences are exact.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return h2_sub((x & 0x000F000Fu) | 0x64006400u, 0x64006400u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t x) { return h2_sub((x & 0x00F000F0u) | 0x54005400u, 0x54005400u); }
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return h2_sub(and_or(x, 0x000F000Fu, 0x64006400u), 0x64006400u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) { return h2_sub(and_or(x, 0x00F000F0u, 0x54005400u), 0x54005400u); }
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -128,6 +147,7 @@ __device__ __forceinline__ uint32_t dup16(__half h) {
     return u | (u << 16);
 }
 __device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return byte_perm(x, x, 0x1010u); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return byte_perm(x, x, 0x3232u); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;

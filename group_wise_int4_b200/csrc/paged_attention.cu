@@ -17,24 +17,41 @@ namespace {
 // ---- few rows: one warp's 16 keys against 8 or 16 query rows ------------------------------
 //
 // mma.sync m16n8k16 with the keys as its 16 rows: a decode step has 1 to 16 query rows per
-// key head, and a 128-row tcgen05 tile would be all padding. Each of 4 warps streams its
-// own keys through its part of a cp.async ring, dequantises in registers and keeps its own
-// maximum, sum and output (a transposed 16 x 8 tile per 16 dims); the warps are joined
-// once at the end. The value product O^T = V^T P^T needs P^T as its 8-column operand,
+// key head, and a 128-row tcgen05 tile would be all padding. A warp is on its own: it
+// streams the codes of one unit and key head through its part of a cp.async ring,
+// dequantises in registers and keeps the maximum, the sum and the output (transposed: 16
+// dims x 8 rows a tile). The value product O^T = V^T P^T needs P^T as its 8-column operand,
 // which movmatrix makes of the score tile; V^T comes from byte permutations of four keys'
-// codes, two keys to a register.
-template <int D, int BITS>
+// codes, two keys to a register. Metadata goes through registers: the lane of a key turns
+// its scales into steps once, for all lanes that use them.
+//
+// Three instructions for two values (extract, subtract the exponent's offset, one fused
+// multiply-add) make about 220 of the 350 that 16 keys of 128 dims take at 4 bits, so the
+// issue slots bound it, not the memory.
+// Warps of a multiprocessor, by registers: without spilling the kernel takes 168 at 8 rows of 128
+// dims (16 warps of 128 registers spill, and take 440 us instead of 338 for a decode step of
+// 144 sequences of 512 to 543 slots, 96 heads), 235 at 16.
+constexpr int rows_warps(int dim, int rows) { return dim == 64 ? (rows == 8 ? 20 : 16) : (rows == 8 ? 12 : 8); }
+
+template <int D, int BITS, int GS, int NR>
 struct RowsShape {
-    static constexpr int KB = D * BITS / 8;                // bytes of a key's codes
-    static constexpr int KW = KB >= 128 ? 16 : 32;         // keys of a warp and stage
-    static constexpr int KEYS = 4 * KW;
-    static constexpr int STAGES = 3;
+    static constexpr int KB = D * BITS / 8, NG = D / GS;   // bytes of a key's codes, groups
+    static constexpr int KW = KB >= 128 ? 16 : 32;         // keys of a stage
+    static constexpr int STAGES = 3;                       // two requested ahead
+    static constexpr int CODE = KW * KB, META = KW * NG * 4;
+    static constexpr int WARP = STAGES * 2 * CODE + 2 * 2 * META;      // shared bytes of a warp
+    static constexpr int WARPS = 2;                        // of a block
+    static constexpr int BLOCKS = rows_warps(D, 8 * NR) / WARPS;
 };
+constexpr int kRowsKeys = 32, kRowsMin = 8;        // a part's granule of keys; a part has at least MIN of them
 
-constexpr int kRowsMin = 2;        // blocks of keys that a part has at least
-
-// 16-byte piece i of a warp's KW keys, in keys' order, is put where the value product reads
-// without bank conflicts: lanes (g, t) read piece(s) g of keys 2t, 2t + 1, ....
+// 16-byte piece c of key `key` of a stage. Keys: pieces in order, except that the odd keys of
+// 128 bytes have theirs swapped in pairs: lanes (g, t) read pieces 2t and 2t + 1 of key g.
+template <int KB>
+__device__ __forceinline__ int key_piece(int key, int c) {
+    return key * (KB / 16) + (KB == 128 ? c ^ (key & 1) : c);
+}
+// Values: lanes (g, t) read piece(s) g of keys 2t, 2t + 1, ... without bank conflicts.
 template <int KB>
 __device__ __forceinline__ int value_piece(int key, int c) {
     if (KB == 128) return key * 8 + (c ^ (((key >> 1) & 3) << 1));
@@ -43,62 +60,99 @@ __device__ __forceinline__ int value_piece(int key, int c) {
 }
 
 template <int D, int BITS, int GS, int NR>
-__global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
-    const PagedView& c = A.c;
-    const RowsPlan& plan = A.plan;
-    const __half *k_new = A.k_new, *v_new = A.v_new;
-    const int64_t kv_stride = A.kv_stride;
-    using S = RowsShape<D, BITS>;
-    constexpr int KB = S::KB, KW = S::KW, KEYS = S::KEYS, ST = S::STAGES;
-    constexpr int NG = D / GS, R = 8 * NR, KT = KW / 16;
-    constexpr int CODE = KW * KB, META = KW * NG * 4, STAGE = 2 * CODE + 2 * META;      // bytes of a warp
+__global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsShape<D, BITS, GS, NR>::BLOCKS)
+    paged_rows_kernel(AttnArgs A) {
+    using S = RowsShape<D, BITS, GS, NR>;
+    constexpr int KB = S::KB, KW = S::KW, ST = S::STAGES, NG = S::NG, R = 8 * NR, KT = KW / 16, CODE = S::CODE;
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int head = blockIdx.x % plan.heads, unit = blockIdx.x / plan.heads;
-    const Unit u = find_unit<R, KEYS, kRowsMin>(c, A.rows, plan, unit);
+    const PagedView& c = A.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int item = blockIdx.x * S::WARPS + warp, share = A.plan.share;
+    const int head = item % A.plan.heads;
+    const Unit u = find_unit<R, kRowsKeys, kRowsMin>(c, A.rows, A.plan, item / A.plan.heads);
+    record_split<R, kRowsKeys>(A, u, item / A.plan.heads, head);
     if (!u.live) return;
-    const int blocks = (u.ctx + KEYS - 1) / KEYS;
-    const int key0 = min(blocks, u.part * u.per) * KEYS;
-    const int key1 = min(u.ctx, min(blocks, (u.part + 1) * u.per) * KEYS);
-    const int stages = (key1 - key0 + KEYS - 1) / KEYS;
-    const int row_end = u.n * plan.share;                // rows of this sequence and key head
-    const int row0 = u.tile * R;
+    const int blocks = (u.ctx + kRowsKeys - 1) / kRowsKeys;
+    const int key0 = min(blocks, u.part * u.per) * kRowsKeys;
+    const int key1 = min(u.ctx, min(blocks, (u.part + 1) * u.per) * kRowsKeys);
+    const int stages = (key1 - key0 + KW - 1) / KW;
+    const int row_end = u.n * share, row0 = u.tile * R;
 
-    const uint32_t my_ring = smem_addr(ring) + warp * ST * STAGE;
-    // lane i of a stage looks up the row of its warp's key i (KW = 16: both halves alike)
-    auto row_index = [&](int s) {
-        const int j = key0 + s * KEYS + warp * KW + (lane & (KW - 1));
-        if (j >= key1) return -1;
-        const int p = page_of(c, u.b, j);
-        return p < 0 ? -1 : slot_row(c, p, head, j);
-    };
-    auto load_stage = [&](int s, int row) {
-        const uint32_t at = my_ring + (s % ST) * STAGE;
+    unsigned char* const mine = ring + warp * S::WARP;
+    uint32_t* const meta = reinterpret_cast<uint32_t*>(mine + ST * 2 * CODE);      // [2][keys, values][KW][NG]
+    const uint32_t my_ring = smem_addr(mine);
+    // Pages hold at least 16 keys: each run of 16 is one contiguous piece of a pool. Runs have a
+    // page (the entry of the table), then a row, one stage after the other, so that nothing
+    // waits for the table.
+    const int32_t* const table_row = c.table + static_cast<int64_t>(u.b) * c.max_pages;
+    auto find_pages = [&](int (&page)[KT], int s) {
 #pragma unroll
-        for (int i = 0; i < CODE / 16 / 32; ++i) {
-            const int piece = lane + i * 32, key = piece / (KB / 16), part = piece % (KB / 16);
-            const int r = __shfl_sync(0xffffffffu, row, key);
-            const int64_t off = r < 0 ? 0 : static_cast<int64_t>(r) * KB + part * 16;
-            cp16(at + piece * 16, c.kc + off, r >= 0);
-            cp16(at + CODE + value_piece<KB>(key, part) * 16, c.vc + off, r >= 0);
-        }
-        if (lane < KW) {                                  // absent keys: min and scale 0, so the values are 0
-            const int64_t off = row < 0 ? 0 : static_cast<int64_t>(row) * NG;
-            cp_small<NG * 4>(at + 2 * CODE + lane * NG * 4, c.km + off, row >= 0);
-            cp_small<NG * 4>(at + 2 * CODE + META + lane * NG * 4, c.vm + off, row >= 0);
+        for (int k = 0; k < KT; ++k) {
+            const int j = key0 + s * KW + k * 16;
+            page[k] = page_entry(c, table_row, j, j < key1);
         }
     };
-    int row_next = stages > 0 ? row_index(0) : -1;
+    auto find_rows = [&](int (&row)[KT], const int (&page)[KT], int s) {
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) {
-        if (s < stages) {
-            const int r = row_next;
-            row_next = s + 1 < stages ? row_index(s + 1) : -1;
-            load_stage(s, r);
+        for (int k = 0; k < KT; ++k) row[k] = entry_row(c, page[k], head, key0 + s * KW + k * 16);
+    };
+    // Whole runs: keys behind the last one lie in the page too, and where there is no page the
+    // stage keeps what it held. Their minimum and step are 0, and so are their values.
+    const uint8_t *const kc = c.kc + lane * 16, *const vc = c.vc + lane * 16;
+    auto load_codes = [&](uint32_t at, const int (&row)[KT]) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            if (row[k] < 0) continue;
+            const int64_t off = static_cast<int64_t>(row[k]) * KB;
+#pragma unroll
+            for (int i = 0; i < KB / 32; ++i) {
+                const int piece = lane + i * 32, key = k * 16 + piece / (KB / 16), part = piece % (KB / 16);
+                cp16(at + key_piece<KB>(key, part) * 16, kc + off + i * 512, true);
+                cp16(at + CODE + value_piece<KB>(key, part) * 16, vc + off + i * 512, true);
+            }
         }
         cp_commit();
+    };
+    // metadata of this lane's key, as {min, scale}: at 32 keys a stage of the key and the value, at 16
+    // of the key (lanes 0-15) or the value
+    constexpr int MS = KW == 32 ? 2 : 1;
+    auto load_meta = [&](uint32_t (&w)[MS][NG], int s, const int (&row)[KT]) {
+        const int key = lane & (KW - 1), r = key < 16 ? row[0] : row[KT - 1];
+        const bool ok = r >= 0 && key0 + s * KW + key < key1;
+        const int64_t off = static_cast<int64_t>(ok ? r + (key & 15) : 0) * NG;
+#pragma unroll
+        for (int k = 0; k < MS; ++k) {
+            const uint32_t* src = (MS == 2 ? k == 1 : lane >= 16) ? c.vm : c.km;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) w[k][i] = ok ? __ldg(src + off + i) : 0u;
+        }
+    };
+    // {min, scale} -> {min, step} in shared memory
+    auto put_meta = [&](const uint32_t (&w)[MS][NG], int s) {
+        uint32_t* dst = meta + (s & 1) * 2 * KW * NG;
+#pragma unroll
+        for (int k = 0; k < MS; ++k) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+                dst[(MS == 2 ? k * KW + lane : lane) * NG + i] =
+                    (w[k][i] & 0xFFFFu) | (static_cast<uint32_t>(__half_as_ushort(step16_of(w[k][i]))) << 16);
+        }
+    };
+
+    int row[KT], page[KT];                                  // of the next stage, of the one whose codes are requested next
+    uint32_t mw[MS][NG];
+    {
+        int p0[KT], p1[KT], r0[KT];
+        find_pages(p0, 0);
+        find_pages(p1, 1);
+        find_pages(page, 2);
+        find_rows(r0, p0, 0);
+        load_codes(my_ring, r0);
+        load_meta(mw, 0, r0);
+        find_rows(row, p1, 1);
+        load_codes(my_ring + 2 * CODE, row);
     }
 
     // queries; the tokens of this lane's score columns (rows 2t, 2t + 1 of each tile)
@@ -108,10 +162,10 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
     for (int n = 0; n < NR; ++n) {
         const int r = row0 + n * 8 + g;
         const bool ok = r < row_end;
-        const int i = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
+        const int i = ok ? r / share : 0, h = ok ? head * share + r % share : 0;
         load_query<D, BITS>(bq[n], A.q + static_cast<int64_t>(u.first + i) * A.q_stride + h * D, t, ok);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) token[n][e] = (row0 + n * 8 + 2 * t + e) / plan.share;
+        for (int e = 0; e < 2; ++e) token[n][e] = (row0 + n * 8 + 2 * t + e) / share;
     }
 
     float m[NR][2], l[NR][2], acc[D / 16][NR][4];
@@ -123,8 +177,10 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
         for (int i = 0; i < D / 16; ++i) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
     }
 
-    // Scores of T tiles of 16 keys (base 2, -inf where hidden) -> running maximum, sum,
-    // and the probabilities as the value product's operand.
+    // Scores of T tiles of 16 keys (-inf where hidden) -> running maximum, sum, and the
+    // probabilities as the value product's operand. The maximum moves only when a score
+    // passes it by more than 2^8: until then probabilities are up to 256, with the same
+    // relative error, and nothing is rescaled.
     auto softmax = [&](auto& sc, auto& pb, auto tiles_c) {
         constexpr int T = decltype(tiles_c)::value;
 #pragma unroll
@@ -135,15 +191,16 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
                 top[e] = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
 #pragma unroll
                 for (int k = 1; k < T; ++k) top[e] = fmaxf(top[e], fmaxf(sc[k][n][e], sc[k][n][2 + e]));
+                top[e] *= kLog2e;
             }
-            if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+            if (__any_sync(0xffffffffu, top[0] > m[n][0] + 8.f || top[1] > m[n][1] + 8.f)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], w));
-                    top[e] = fmaxf(top[e], m[n][e]);
-                    const float f = exp2_fast(m[n][e] - top[e]);
-                    m[n][e] = top[e];
+                    const bool moves = top[e] > m[n][e] + 8.f;      // a row's result depends on no other row
+                    const float f = moves ? exp2_fast(m[n][e] - top[e]) : 1.f;
+                    m[n][e] = moves ? top[e] : m[n][e];
                     l[n][e] *= f;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -156,7 +213,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
             for (int k = 0; k < T; ++k) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(sc[k][n][e] - m[n][e & 1]);
+                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(sc[k][n][e], kLog2e, -m[n][e & 1]));
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];
                 pb[k][n][0] = mat_trans(half2_of(p[0], p[1]));
@@ -165,12 +222,13 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
         }
     };
 
-    // ---- fresh keys, by the last part: tile after tile of 16, shared out to the warps
-    if (k_new != nullptr && u.part == u.parts - 1) {
-        const int last = min(u.n, (min(row_end, row0 + R) - 1) / plan.share + 1);       // keys any row sees
-        const __half* kf = k_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
-        const __half* vf = v_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
-        for (int j0 = warp * 16; j0 < last; j0 += 64) {
+    // ---- fresh keys, by the last part
+    if (A.k_new != nullptr && u.part == u.parts - 1) {
+        const int last = (min(row_end, row0 + R) - 1) / share + 1;          // keys any row sees
+        const int64_t kv_stride = A.kv_stride;
+        const __half* kf = A.k_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
+        const __half* vf = A.v_new + static_cast<int64_t>(u.first) * kv_stride + head * D;
+        for (int j0 = 0; j0 < last; j0 += 16) {
             float sc[1][NR][4];
 #pragma unroll
             for (int n = 0; n < NR; ++n) sc[0][n][0] = sc[0][n][1] = sc[0][n][2] = sc[0][n][3] = 0.f;
@@ -194,7 +252,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = j0 + g + (e >> 1) * 8;
-                    sc[0][n][e] = j < last && j <= token[n][e & 1] ? sc[0][n][e] * kLog2e : -INFINITY;
+                    if (j >= last || j > token[n][e & 1]) sc[0][n][e] = -INFINITY;
                 }
             uint32_t pb[1][NR][2];
             softmax(sc, pb, std::integral_constant<int, 1>{});
@@ -255,41 +313,44 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
 
     // ---- cached keys
     const int kgrp = t * (D / 4) / GS, vgrp = g * (D / 8) / GS;     // group of this lane's dims
+    int now = 0, ahead = 2 * 2 * CODE;    // stages in the ring: this one, the one requested
     for (int s = 0; s < stages; ++s) {
+        put_meta(mw, s);
         cp_wait<ST - 2>();
         __syncwarp();                     // the stage has landed for, and the one before it is read by, every lane
-        if (s + ST - 1 < stages) {
-            const int r = row_next;
-            row_next = s + ST < stages ? row_index(s + ST) : -1;
-            load_stage(s + ST - 1, r);
-        }
-        cp_commit();
-        const int j0 = key0 + s * KEYS + warp * KW;
-        if (j0 >= key1) continue;
-        const unsigned char* st = ring + warp * ST * STAGE + (s % ST) * STAGE;
-        const uint32_t* kmeta = reinterpret_cast<const uint32_t*>(st + 2 * CODE);
-        const uint32_t* vmeta = reinterpret_cast<const uint32_t*>(st + 2 * CODE + META);
+        load_meta(mw, s + 1, row);
+        find_rows(row, page, s + 2);
+        load_codes(my_ring + ahead, row);
+        find_pages(page, s + 3);
+        const int j0 = key0 + s * KW;
+        const unsigned char* st = mine + now;
+        now = now == 2 * 2 * CODE ? 0 : now + 2 * CODE;
+        ahead = ahead == 2 * 2 * CODE ? 0 : ahead + 2 * CODE;
+        const uint32_t* kmeta = meta + (s & 1) * 2 * KW * NG;
+        const uint32_t* vmeta = kmeta + KW * NG;
         float sc[KT][NR][4];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) sc[k][n][0] = sc[k][n][1] = sc[k][n][2] = sc[k][n][3] = 0.f;
             uint32_t x0[KB / 16], x8[KB / 16];
-            const unsigned char* kc = st + (k * 16 + g) * KB + t * (KB / 4);
 #pragma unroll
             for (int w = 0; w < KB / 16; w += (KB >= 64 ? 4 : 2)) {
                 if (KB >= 64) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(kc + w * 4), z = *reinterpret_cast<const uint4*>(kc + 8 * KB + w * 4);
+                    constexpr int PER = KB / 64;           // pieces of a lane
+                    const uint4 a = *reinterpret_cast<const uint4*>(st + key_piece<KB>(k * 16 + g, t * PER + w / 4) * 16);
+                    const uint4 z = *reinterpret_cast<const uint4*>(st + key_piece<KB>(k * 16 + g + 8, t * PER + w / 4) * 16);
                     x0[w] = a.x; x0[(w + 1) % (KB / 16)] = a.y; x0[(w + 2) % (KB / 16)] = a.z; x0[(w + 3) % (KB / 16)] = a.w;
                     x8[w] = z.x; x8[(w + 1) % (KB / 16)] = z.y; x8[(w + 2) % (KB / 16)] = z.z; x8[(w + 3) % (KB / 16)] = z.w;
                 } else {
+                    const unsigned char* kc = st + (k * 16 + g) * KB + t * (KB / 4);
                     const uint2 a = *reinterpret_cast<const uint2*>(kc + w * 4), z = *reinterpret_cast<const uint2*>(kc + 8 * KB + w * 4);
                     x0[w] = a.x; x0[(w + 1) % (KB / 16)] = a.y;
                     x8[w] = z.x; x8[(w + 1) % (KB / 16)] = z.y;
                 }
             }
             const uint32_t m0 = kmeta[(k * 16 + g) * NG + kgrp], m8 = kmeta[(k * 16 + g + 8) * NG + kgrp];
-            const uint32_t st0 = dup16(step16_of(m0)), st8 = dup16(step16_of(m8)), mn0 = dup_lo(m0), mn8 = dup_lo(m8);
+            const uint32_t st0 = dup_hi(m0), st8 = dup_hi(m8), mn0 = dup_lo(m0), mn8 = dup_lo(m8);
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
                 uint32_t a[4], z[4];
@@ -303,13 +364,13 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
                     mma168(sc[k][n], a1, bq[n][2 * w + 1][0], bq[n][2 * w + 1][1]);
                 }
             }
-            const bool in0 = j0 + k * 16 + g < key1, in8 = j0 + k * 16 + g + 8 < key1;
+            if (j0 + KW > key1) {
+                const bool in0 = j0 + k * 16 + g < key1, in8 = j0 + k * 16 + g + 8 < key1;
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                sc[k][n][0] = in0 ? sc[k][n][0] * kLog2e : -INFINITY;
-                sc[k][n][1] = in0 ? sc[k][n][1] * kLog2e : -INFINITY;
-                sc[k][n][2] = in8 ? sc[k][n][2] * kLog2e : -INFINITY;
-                sc[k][n][3] = in8 ? sc[k][n][3] * kLog2e : -INFINITY;
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(e < 2 ? in0 : in8)) sc[k][n][e] = -INFINITY;
             }
         }
         uint32_t pb[KT][NR][2];
@@ -323,8 +384,7 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
             for (int p = 0; p < 2; ++p) {
                 const int key = k * 16 + 2 * t + 8 * p;
                 const uint32_t ma = vmeta[key * NG + vgrp], mz = vmeta[(key + 1) * NG + vgrp];
-                step[p] = static_cast<uint32_t>(__half_as_ushort(step16_of(ma))) |
-                          (static_cast<uint32_t>(__half_as_ushort(step16_of(mz))) << 16);
+                step[p] = byte_perm(ma, mz, 0x7632u);
                 mn[p] = byte_perm(ma, mz, 0x5410u);
             }
 #pragma unroll
@@ -346,8 +406,6 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
             for (int i = 0; i < D / 16; ++i) {             // dims 2i and 2i + 1 of this lane's D/8
                 uint32_t a[4];
                 if (BITS == 4) {
-                    constexpr int dummy = 0;
-                    (void)dummy;
                     const uint32_t sel = (i % 4) * 0x11u + (4 + i % 4) * 0x1100u;
                     const uint32_t y0 = byte_perm(x[0][i / 4 % VW], x[1][i / 4 % VW], sel);
                     const uint32_t y1 = byte_perm(x[2][i / 4 % VW], x[3][i / 4 % VW], sel);
@@ -371,58 +429,36 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(AttnArgs A) {
         }
     }
     cp_wait<0>();
-    __syncthreads();                      // every warp is done with the ring, which now takes the outputs
 
-    // ---- join the warps
-    float* so = reinterpret_cast<float*>(ring);            // [4][R][D]
-    __shared__ float sm[4][R], sl[4][R];
+    // lane (g, t): rows 2t, 2t + 1 of each tile, dims [g D/8, (g + 1) D/8)
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float s = l[n][e];
+            float sum = l[n][e];
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+            for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             const int r = n * 8 + 2 * t + e;
-            if (g == 0) {
-                sm[warp][r] = m[n][e];
-                sl[warp][r] = s;
+            if (row0 + r >= row_end) continue;
+            if (u.parts == 1) {
+                const int64_t at = static_cast<int64_t>(u.first + token[n][e]) * (A.plan.heads * share) + head * share + (row0 + r) % share;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                uint32_t w[D / 16];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) w[i] = half2_of(acc[i][n][e] * inv, acc[i][n][2 + e] * inv);
+#pragma unroll
+                for (int i = 0; i < D / 16; i += 4)
+                    *reinterpret_cast<uint4*>(A.o + at * D + g * (D / 8) + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                if (g == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (m[n][e] + log2f(sum)) * kLn2;
+            } else if (u.slot < A.slots) {
+                float* p = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + r) * (D + 4);
+#pragma unroll
+                for (int i = 0; i < D / 16; i += 2)
+                    *reinterpret_cast<float4*>(p + g * (D / 8) + 2 * i) =
+                        make_float4(acc[i][n][e], acc[i][n][2 + e], acc[i + 1][n][e], acc[i + 1][n][2 + e]);
+                if (g == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[n][e], sum);
             }
-            float* dst = so + (warp * R + r) * D + g * (D / 8);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][n][e], acc[i][n][2 + e]);
         }
-    __syncthreads();
-    for (int i = tid; i < R * (D / 4); i += 128) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        if (row0 + r >= row_end) continue;
-        float top = -FLT_MAX;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[w][r]);
-        float sum = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = exp2_fast(sm[w][r] - top);
-            const float4 x = *reinterpret_cast<const float4*>(so + (w * R + r) * D + d);
-            sum = fmaf(f, sl[w][r], sum);
-            a.x = fmaf(f, x.x, a.x);
-            a.y = fmaf(f, x.y, a.y);
-            a.z = fmaf(f, x.z, a.z);
-            a.w = fmaf(f, x.w, a.w);
-        }
-        if (u.parts == 1) {
-            const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
-            const int64_t at = static_cast<int64_t>(u.first + tok) * (plan.heads * plan.share) + h;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-            if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        } else if (u.slot < A.slots) {
-            float* p = A.parts + ((static_cast<int64_t>(u.slot) * plan.heads + head) * R + r) * (D + 4);
-            *reinterpret_cast<float4*>(p + d) = a;
-            if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(top, sum);
-        }
-    }
 }
 
 // ---- accumulated weights ------------------------------------------------------------------
@@ -567,8 +603,8 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
 
 struct AttnPlan {
     int share, row_tile, target, slots;
-    int64_t units, parts_bytes, lse_bytes;
-    int64_t bytes() const { return parts_bytes + lse_bytes; }
+    int64_t units, records_bytes, parts_bytes, lse_bytes;
+    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes; }
 };
 
 inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -578,12 +614,13 @@ AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total,
     p.share = n_heads / c->n_kv_heads;
     const int64_t rows = static_cast<int64_t>(most) * p.share;
     p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
-    // blocks wanted on the device at once: 4 a multiprocessor
-    p.target = p.row_tile <= 16 ? 4 * sm_count() : paged_tile_target(p.row_tile, c->head_dim);
+    // units times heads wanted: what the device holds at once
+    p.target = p.row_tile <= 16 ? rows_warps(c->head_dim, p.row_tile) * sm_count() : paged_tile_target(p.row_tile, c->head_dim);
     // every sequence's row tiles, and what their parts add (the bounds stand at find_unit)
     const int64_t more = (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
     p.units = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch + more;
     p.slots = static_cast<int>(2 * more);
+    p.records_bytes = 256 + up256(static_cast<int64_t>(p.slots) * sizeof(SplitRecord));
     p.parts_bytes = up256(static_cast<int64_t>(p.slots) * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
     p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
     return p;
@@ -649,22 +686,25 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     a.kv_stride = kv_stride;
     a.o = static_cast<__half*>(o);
     unsigned char* w = static_cast<unsigned char*>(ws);
-    a.parts = reinterpret_cast<float*>(w);
-    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.parts_bytes) : lse;
+    a.split_units = reinterpret_cast<int*>(w);
+    a.records = reinterpret_cast<SplitRecord*>(w + 256);
+    a.parts = reinterpret_cast<float*>(w + p.records_bytes);
+    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes) : lse;
     a.slots = p.slots;
     const cudaStream_t st = as_stream(stream);
-    const dim3 grid(static_cast<unsigned>(p.units * kvh));
     const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;
     if (p.row_tile > 16) {
         launch_paged_tile(a, D, B, G, p.row_tile, p.units, st);
     } else {
 #define ROWS(D_, B_, G_, N_)                                                                                        \
     do {                                                                                                            \
-        constexpr int ring = RowsShape<D_, B_>::STAGES * 4 * RowsShape<D_, B_>::KW * 2 * (RowsShape<D_, B_>::KB + D_ / G_ * 4); \
-        constexpr int outs = 4 * 8 * N_ * D_ * 4, smem = ring > outs ? ring : outs;                                 \
-        set_smem_once(paged_rows_kernel<D_, B_, G_, N_>, smem);                                                     \
-        launch_k(paged_rows_kernel<D_, B_, G_, N_>, grid, dim3(128), smem, st, true, a);                            \
-        launch_join<D_, 8 * N_, RowsShape<D_, B_>::KEYS, kRowsMin>(a, st);                                          \
+        using S = RowsShape<D_, B_, G_, N_>;                                                             \
+        constexpr int smem = S::WARPS * S::WARP;                                                         \
+        set_smem_once(paged_rows_kernel<D_, B_, G_, N_>, smem);                                          \
+        const int64_t items = p.units * kvh;                                                             \
+        launch_k(paged_rows_kernel<D_, B_, G_, N_>, dim3(static_cast<unsigned>((items + S::WARPS - 1) / S::WARPS)), \
+                 dim3(S::WARPS * 32), smem, st, true, a);                                                \
+        launch_join<D_, 8 * N_, kRowsKeys, kRowsMin>(a, st);                                             \
     } while (0)
 #define ROWS_N(D_, B_, G_) \
     do { if (p.row_tile == 8) ROWS(D_, B_, G_, 1); else ROWS(D_, B_, G_, 2); } while (0)

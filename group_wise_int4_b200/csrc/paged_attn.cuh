@@ -121,7 +121,7 @@ __device__ __forceinline__ uint4 without_wild(uint4 x) {
 // shuffles), so nothing has to be planned on the host or in another launch.
 //
 // Bounds that the workspace relies on, with work = sum of row tiles times key blocks and
-// per >= work * heads / target: tiles are at most total * share / R + batch; the parts
+// per >= work * heads / target (target: of units times heads): tiles are at most total * share / R + batch; the parts
 // beyond each tile's first at most work / per <= target / heads; and the units of tiles
 // that are split (ceil(blocks / per) < 2 blocks / per, as blocks > per) fewer than
 // 2 target / heads: only those have a slot for partial results.
@@ -131,29 +131,36 @@ struct RowsPlan {
 
 struct Unit {
     int b, tile, part, parts, per;      // per: key blocks in a part
+    int plan_per;                       // the whole batch's, before the parts of a tile are made even
     int slot;                           // of this unit's partial result, where parts > 1
     int first, n, ctx;
     bool live;
 };
 
 // MIN: blocks of keys that a part has at least; less costs more to join than it saves.
-// SPLIT: `unit` counts the units of split tiles alone (it is a partial slot).
-template <int R, int KEYS, int MIN, bool SPLIT = false>
+template <int R, int KEYS, int MIN>
 __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
     const int lane = threadIdx.x & 31;
-    // work of the whole batch, in key blocks times row tiles
-    int64_t work = 0;
+    // work of the whole batch, in key blocks times row tiles, and the row tiles
+    int64_t work = 0, all = 0;
     for (int b = lane; b < p.batch; b += 32) {
         int first;
         const int n = rows_of(rows, b, first, c.status);
         const int64_t tiles = (static_cast<int64_t>(n) * p.share + R - 1) / R;
         work += tiles * ((slots_of(c, b) + KEYS - 1) / KEYS);
+        all += tiles;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
-    const int64_t even = (work * p.heads + p.target - 1) / p.target;
+    for (int o = 16; o > 0; o >>= 1) {
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    // With room for every tile's first part beside them the parts fit the target: they run at
+    // once. Many tiles need no such care.
+    const int64_t fit = p.target - all * p.heads, room = fit > p.target / 2 ? fit : p.target;
+    const int64_t even = (work * p.heads + room - 1) / room;
     Unit u{};
-    u.per = static_cast<int>(even < MIN ? MIN : even > (1 << 30) ? (1 << 30) : even);
+    u.plan_per = static_cast<int>(even < MIN ? MIN : even > (1 << 30) ? (1 << 30) : even);
     int64_t before = 0, split = 0;                      // units, and units of split tiles, of the sequences passed
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
@@ -162,41 +169,48 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
             n = rows_of(rows, b, first, c.status);
             ctx = slots_of(c, b);
             tiles = static_cast<int>((static_cast<int64_t>(n) * p.share + R - 1) / R);
-            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.per - 1) / u.per);
+            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per);
         }
-        const int64_t mine = static_cast<int64_t>(tiles) * parts, mine2 = parts > 1 ? mine : 0;
-        int64_t x = mine, y = mine2;
+        // (more units than 2^25 of one sequence would be more than a launch has)
+        const int mine = static_cast<int>(min(static_cast<int64_t>(tiles) * parts, static_cast<int64_t>(1 << 25)));
+        const int mine2 = parts > 1 ? mine : 0;
+        const int sum = __reduce_add_sync(0xffffffffu, mine), sum2 = __reduce_add_sync(0xffffffffu, mine2);
+        if (unit >= before + sum) {
+            before += sum;
+            split += sum2;
+            continue;
+        }
+        int x = mine, y = mine2;                        // up to and with b
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t xx = __shfl_up_sync(0xffffffffu, x, o), yy = __shfl_up_sync(0xffffffffu, y, o);
+            const int xx = __shfl_up_sync(0xffffffffu, x, o), yy = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) {
                 x += xx;
                 y += yy;
             }
         }
-        x += before;                                    // up to and with b
-        y += split;
-        const unsigned has = __ballot_sync(0xffffffffu, unit < (SPLIT ? y : x));
-        if (has) {
-            const int l = __ffs(has) - 1;
-            const int at = static_cast<int>(unit - __shfl_sync(0xffffffffu, SPLIT ? y - mine2 : x - mine, l));
-            u.b = b0 + l;
-            u.n = __shfl_sync(0xffffffffu, n, l);
-            u.ctx = __shfl_sync(0xffffffffu, ctx, l);
-            u.first = __shfl_sync(0xffffffffu, first, l);
-            u.parts = __shfl_sync(0xffffffffu, parts, l);
-            u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
-            u.slot = static_cast<int>(__shfl_sync(0xffffffffu, y - mine2, l)) + at;
-            u.tile = at / u.parts;
-            u.part = at % u.parts;
-            u.live = true;
-            return u;
-        }
-        before = __shfl_sync(0xffffffffu, x, 31);
-        split = __shfl_sync(0xffffffffu, y, 31);
+        const int want = static_cast<int>(unit - before);
+        const int l = __ffs(__ballot_sync(0xffffffffu, want < x)) - 1;
+        const int at = want - __shfl_sync(0xffffffffu, x - mine, l);
+        u.b = b0 + l;
+        u.n = __shfl_sync(0xffffffffu, n, l);
+        u.ctx = __shfl_sync(0xffffffffu, ctx, l);
+        u.first = __shfl_sync(0xffffffffu, first, l);
+        u.parts = __shfl_sync(0xffffffffu, parts, l);
+        u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
+        u.slot = static_cast<int>(split) + __shfl_sync(0xffffffffu, y - mine2, l) + at;
+        u.tile = at / u.parts;
+        u.part = at % u.parts;
+        u.live = true;
+        return u;
     }
     return u;
 }
+
+// What a split unit tells the joining launch, at its partial slot.
+struct SplitRecord {
+    int b, tile, part, parts;
+};
 
 // What a launch of either attention kernel gets. Partial results: [slot][head][row of the
 // tile][D + 4]: the output, then the maximum (base 2) and the sum.
@@ -211,47 +225,106 @@ struct AttnArgs {
     __half* o;
     float* lse;
     float* parts;
+    int* split_units;           // how many partial slots are in use
+    SplitRecord* records;       // [slots]
     int slots;                  // of partial results
 };
 
-// Joins the parts of split tiles. Block (slot, head, z): the rows of the slot's tile are
-// shared out evenly over its parts' slots and z, so that every block reads about as much.
-template <int D, int R, int KEYS, int MIN>
+// Called by one warp of every unit and head: unit 0 says how many partial slots there are, a
+// split unit where it belongs.
+template <int R, int KEYS>
+__device__ __forceinline__ void record_split(const AttnArgs& A, const Unit& u, int unit, int head) {
+    const int lane = threadIdx.x & 31;
+    if (head != 0) return;
+    if (unit == 0) {
+        int64_t units = 0;
+        for (int b = lane; b < A.plan.batch; b += 32) {
+            int first;
+            const int n = rows_of(A.rows, b, first, A.c.status);
+            const int64_t tiles = (static_cast<int64_t>(n) * A.plan.share + R - 1) / R;
+            const int parts = ((slots_of(A.c, b) + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per;
+            if (parts > 1) units += tiles * parts;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+        if (lane == 0) *A.split_units = static_cast<int>(min(units, static_cast<int64_t>(A.slots)));
+    }
+    if (lane == 0 && u.live && u.parts > 1 && u.slot < A.slots) A.records[u.slot] = SplitRecord{u.b, u.tile, u.part, u.parts};
+}
+
+// Joins the parts of split tiles. A block goes through slots and heads; the rows of a slot's
+// tile are shared out evenly over its parts' slots and over z.
+template <int D, int R>
 __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
     pdl_wait();
     pdl_trigger();
     const RowsPlan& plan = A.plan;
-    const int head = blockIdx.x % plan.heads;
-    const Unit u = find_unit<R, KEYS, MIN, true>(A.c, A.rows, plan, blockIdx.x / plan.heads);
-    if (!u.live || u.slot - u.part + u.parts > A.slots) return;
-    const int row0 = u.tile * R, rows = min(R, u.n * plan.share - row0);
-    const int chunks = u.parts * gridDim.y, chunk = u.part * gridDim.y + blockIdx.y, per = (rows + chunks - 1) / chunks;
-    constexpr int L = D / 4;                            // lanes of a row
-    const int d = (threadIdx.x % L) * 4;
-    const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
-    for (int r = chunk * per + threadIdx.x / L; r < min(rows, (chunk + 1) * per); r += 128 / L) {
-        const float* p = A.parts + ((static_cast<int64_t>(u.slot - u.part) * plan.heads + head) * R + r) * (D + 4);
-        float top = -FLT_MAX;
-#pragma unroll 8
-        for (int k = 0; k < u.parts; ++k) top = fmaxf(top, __ldg(p + k * step + D));
-        float sum = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < u.parts; ++k) {
-            const float2 ml = __ldg(reinterpret_cast<const float2*>(p + k * step + D));
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + k * step + d));
-            const float f = exp2_fast(ml.x - top);
-            sum = fmaf(f, ml.y, sum);
-            a.x = fmaf(f, x.x, a.x);
-            a.y = fmaf(f, x.y, a.y);
-            a.z = fmaf(f, x.z, a.z);
-            a.w = fmaf(f, x.w, a.w);
+    const int items = min(*A.split_units, A.slots) * plan.heads;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int head = item % plan.heads, slot = item / plan.heads;
+        const SplitRecord rec = A.records[slot];
+        // offsets that overlap (cu out of order) can leave a record unset: whatever it holds, nothing
+        // outside the slots and the sequence's rows is touched
+        if (static_cast<unsigned>(rec.b) >= static_cast<unsigned>(plan.batch) || rec.part < 0 || rec.part > slot || rec.tile < 0 ||
+            rec.parts <= rec.part || rec.parts > A.slots || slot - rec.part > A.slots - rec.parts)
+            continue;
+        int first;
+        const int row_end = rows_of(A.rows, rec.b, first, A.c.status) * plan.share;
+        if (rec.tile >= (row_end + R - 1) / R) continue;
+        const int row0 = rec.tile * R, rows = min(R, row_end - row0);
+        const int chunks = rec.parts * gridDim.y, chunk = rec.part * gridDim.y + blockIdx.y, per = (rows + chunks - 1) / chunks;
+        constexpr int L = D / 4, G = 128 / L;               // threads of a row, groups of them
+        const int d = (threadIdx.x % L) * 4, group = threadIdx.x / L;
+        const int64_t step = static_cast<int64_t>(plan.heads) * R * (D + 4);
+        const int begin = chunk * per, end = min(rows, begin + per);
+        if (begin >= end) continue;
+        // enough rows: one a group; few (long sequences with many parts): the groups share a row's parts
+        const bool share_row = end - begin < G;
+        __shared__ float4 part_out[G][L];
+        __shared__ float2 part_stat[G];
+        for (int r = begin + (share_row ? 0 : group); r < end; r += share_row ? 1 : G) {
+            const float* p = A.parts + ((static_cast<int64_t>(slot - rec.part) * plan.heads + head) * R + r) * (D + 4);
+            float top = -FLT_MAX, sum = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto add = [&](float2 ml, float4 x) {
+                const float t = fmaxf(top, ml.x), f0 = exp2_fast(top - t), f = exp2_fast(ml.x - t);
+                top = t;
+                sum = fmaf(sum, f0, f * ml.y);
+                a.x = fmaf(a.x, f0, f * x.x);
+                a.y = fmaf(a.y, f0, f * x.y);
+                a.z = fmaf(a.z, f0, f * x.z);
+                a.w = fmaf(a.w, f0, f * x.w);
+            };
+            const int by = share_row ? G : 1;
+            for (int k0 = share_row ? group : 0; k0 < rec.parts; k0 += 8 * by) {
+                float2 ml[8];
+                float4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = k0 + i * by;
+                    if (k >= rec.parts) break;
+                    ml[i] = __ldg(reinterpret_cast<const float2*>(p + k * step + D));
+                    x[i] = __ldg(reinterpret_cast<const float4*>(p + k * step + d));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (k0 + i * by < rec.parts) add(ml[i], x[i]);
+            }
+            if (share_row) {
+                __syncthreads();                            // (the row before is read)
+                part_out[group][threadIdx.x % L] = a;
+                if (d == 0) part_stat[group] = make_float2(top, sum);
+                __syncthreads();
+                if (group != 0) continue;
+#pragma unroll
+                for (int i = 1; i < G; ++i) add(part_stat[i], part_out[i][threadIdx.x]);
+            }
+            const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
+            const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
+            if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
-        const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
-        const int64_t at = static_cast<int64_t>(u.first + tok) * (plan.heads * plan.share) + h;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-        if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -260,8 +333,10 @@ __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
 template <int D, int R, int KEYS, int MIN>
 void launch_join(const AttnArgs& a, cudaStream_t st) {
     if (static_cast<int64_t>(a.c.max_pages) << a.c.shift <= static_cast<int64_t>(MIN) * KEYS) return;
-    launch_k(paged_join_kernel<D, R, KEYS, MIN>, dim3(static_cast<unsigned>(a.slots * a.plan.heads), R <= 16 ? 1 : R / 32),
-             dim3(128), 0, st, true, a);
+    const int64_t items = static_cast<int64_t>(a.slots) * a.plan.heads;
+    const int fill = 8 * sm_count();                    // blocks of a device that is full
+    launch_k(paged_join_kernel<D, R>, dim3(static_cast<unsigned>(items < fill ? items : fill), R <= 16 ? 1 : R / 64), dim3(128), 0, st,
+             true, a);
 }
 
 // The tcgen05 kernel over tiles of paged_tile_rows() query rows; `units` blocks per key head.

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     pdl_trigger();
     const int head = blockIdx.x % A.plan.heads;
     const Unit u = find_unit<R, 128, kTileMin>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
+    if (warp == 0) record_split<R, 128>(A, u, blockIdx.x / A.plan.heads, head);
     if (!u.live) return;
     const int share = A.plan.share;
     const int blocks = (u.ctx + 127) / 128;
@@ -313,12 +314,13 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         const uint8_t* codes = second ? c.vc : c.kc;
         const uint32_t* metas = second ? c.vm : c.km;
         const uint32_t dst = second ? sv : sk, full = second ? v_full : k_full, empty = second ? v_empty : k_empty;
-        auto row_index = [&](int j) {
+        // the table's entry, the codes and their conversion: each a block of keys after the other
+        const int32_t* const table_row = c.table + static_cast<int64_t>(u.b) * c.max_pages;
+        auto find_page = [&](int j) {
             const int k = key0 + j * NK + key;
-            if (j >= nc || k >= key1) return -1;
-            const int p = page_of(c, u.b, k);
-            return p < 0 ? -1 : slot_row(c, p, head, k);
+            return page_entry(c, table_row, k, k < key1);
         };
+        auto find_row = [&](int page, int j) { return entry_row(c, page, head, key0 + j * NK + key); };
         auto load = [&](uint4 (&x)[NX], uint32_t (&meta)[NG], int row) {
             const uint4* src = reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row < 0 ? 0 : row) * KB);
 #pragma unroll
@@ -358,12 +360,13 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         };
         uint4 x[2][NX];
         uint32_t meta[2][NG];
-        load(x[0], meta[0], row_index(0));
-        int row = row_index(1);
+        const int page0 = find_page(0);
+        int page = find_page(1);
+        load(x[0], meta[0], find_row(page0, 0));
         auto step = [&](int j, auto now_c) {
             constexpr int NOW = decltype(now_c)::value;
-            load(x[1 - NOW], meta[1 - NOW], row);
-            row = row_index(j + 2);
+            load(x[1 - NOW], meta[1 - NOW], find_row(page, j + 1));
+            page = find_page(j + 2);
             if (!(ok = slot_free(j))) return;
             convert(x[NOW], meta[NOW], dst + (j % ST) * T::BLOCK);
             publish(j);
