@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int item = blockIdx.x * S::WARPS + warp, share = A.plan.share;
     const int head = item % A.plan.heads;
-    const Unit u = find_unit<R, kRowsKeys, kRowsMin>(c, A.rows, A.plan, item / A.plan.heads);
+    const Unit u = find_unit<R, kRowsKeys, kRowsMin, 1>(c, A.rows, A.plan, item / A.plan.heads);
     record_split<R, kRowsKeys>(A, u, item / A.plan.heads, head);
     if (!u.live) return;
     const int blocks = (u.ctx + kRowsKeys - 1) / kRowsKeys;
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     };
 
     int row[KT], page[KT];                                  // of the next stage, of the one whose codes are requested next
+    int before[KT];                                         // rows of the stage before that
     uint32_t mw[MS][NG];
     {
         int p0[KT], p1[KT], r0[KT];
@@ -151,6 +152,8 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
         find_rows(r0, p0, 0);
         load_codes(my_ring, r0);
         load_meta(mw, 0, r0);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) before[k] = r0[k];
         find_rows(row, p1, 1);
         load_codes(my_ring + 2 * CODE, row);
     }
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
                     const int j = j0 + g + (e >> 1) * 8;
                     if (j >= last || j > token[n][e & 1]) sc[0][n][e] = -INFINITY;
                 }
+            if (NR == 1 && A.fresh != nullptr && lane == 0) A.fresh[u.b * A.plan.heads + head] = sc[0][0][0];
             uint32_t pb[1][NR][2];
             softmax(sc, pb, std::integral_constant<int, 1>{});
             uint4 x[4][D / 64];
@@ -318,6 +322,12 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
         put_meta(mw, s);
         cp_wait<ST - 2>();
         __syncwarp();                     // the stage has landed for, and the one before it is read by, every lane
+        int here[KT];                     // rows of this stage
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            here[k] = before[k];
+            before[k] = row[k];
+        }
         load_meta(mw, s + 1, row);
         find_rows(row, page, s + 2);
         load_codes(my_ring + ahead, row);
@@ -363,6 +373,10 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
                     mma168(sc[k][n], a0, bq[n][2 * w][0], bq[n][2 * w][1]);
                     mma168(sc[k][n], a1, bq[n][2 * w + 1][0], bq[n][2 * w + 1][1]);
                 }
+            }
+            if (NR == 1 && A.scores != nullptr && t == 0 && here[k] >= 0) {
+                A.scores[here[k] + g] = sc[k][0][0];         // (a whole run lies in the page)
+                A.scores[here[k] + g + 8] = sc[k][0][2];
             }
             if (j0 + KW > key1) {
                 const bool in0 = j0 + k * 16 + g < key1, in8 = j0 + k * 16 + g + 8 < key1;
@@ -463,10 +477,48 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 
 // ---- accumulated weights ------------------------------------------------------------------
 //
-// weight[slot] += sum over rows of exp(s - lse): the scores again, now with the rows' final
-// statistics. A warp holds 32 keys as operands in registers and goes through all query
-// rows of the sequence, so every key's sum stays in its lanes and is added in one fixed
-// order; no atomics. Query rows pass through shared memory, 32 at a time, for 4 warps.
+// weight[slot] += sum over rows of exp(s - lse), with the rows' final statistics.
+//
+// One row (a decode step without shared heads): the attention kernel leaves its scores, 4
+// bytes a slot, and this pass reads them and updates the weights: 12 bytes a slot instead
+// of the codes and their conversion again (32 sequences of 500 to 1999 slots, 32 heads of
+// 64: 72 us with the kernel below).
+__global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
+    pdl_wait();
+    pdl_trigger();
+    const PagedView& c = A.c;
+    const int head = blockIdx.y, b = blockIdx.z;
+    int first;
+    if (rows_of(A.rows, b, first, c.status) == 0) return;
+    const int ctx = slots_of(c, b), held = ctx + (A.fresh != nullptr && A.k_new != nullptr);
+    const int s0 = (blockIdx.x * 128 + threadIdx.x) * 4;      // four slots of one page
+    if (s0 >= held) return;
+    if (s0 >= paged_capacity(c)) {
+        paged_bad(c);                                         // no slot for the new token
+        return;
+    }
+    const int p = page_of(c, b, s0);
+    if (p < 0) return;
+    const int64_t row = slot_row(c, p, head, s0);
+    const float norm = __ldg(A.lse + static_cast<int64_t>(first) * A.plan.heads + head) * kLog2e;
+    const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
+    float4 w = *reinterpret_cast<const float4*>(c.weight + row);
+    const float fresh = s0 + 4 > ctx && held > ctx ? exp2_fast(fmaf(A.fresh[b * A.plan.heads + head], kLog2e, -norm)) : 0.f;
+    auto one = [&](float& x, float score, int s) {
+        if (s < ctx) x += exp2_fast(fmaf(score, kLog2e, -norm));
+        else if (s < held) x = fresh;
+    };
+    one(w.x, sc.x, s0);
+    one(w.y, sc.y, s0 + 1);
+    one(w.z, sc.z, s0 + 2);
+    one(w.w, sc.w, s0 + 3);
+    *reinterpret_cast<float4*>(c.weight + row) = w;
+}
+
+// Any number of rows: the scores again. A warp holds 32 keys as operands in registers and goes
+// through all query rows of the sequence, so every key's sum stays in its lanes and is added
+// in one fixed order; no atomics. Query rows pass through shared memory, 32 at a time, for 4
+// warps.
 template <int D, int BITS, int GS>
 __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     const PagedView& c = A.c;
@@ -488,6 +540,24 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     const int j0 = (static_cast<int>(blockIdx.x) - (fresh ? old_blocks : 0)) * 128 + warp * 32;    // slot, or fresh token
     const int jend = fresh ? (k_new ? n : 0) : ctx;
     if (j0 - warp * 32 >= jend || n == 0) return;       // a sequence without new tokens keeps its weights
+    // rows of the tokens that see any of the block's keys
+    const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
+    const int tiles = (row_end - row_lo + QR - 1) / QR;
+    auto load_rows = [&](int s) {
+        for (int i = tid; i < QR * (D / 8); i += 128) {
+            const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
+            const bool ok = r < row_end;
+            const int tok = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
+            cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
+        }
+        if (tid < QR) {
+            const int r = row_lo + s * QR + tid;
+            const int tok = r / plan.share, h = head * plan.share + r % plan.share;
+            sl[s & 1][tid] = r < row_end ? __ldg(lse + static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h) * kLog2e : INFINITY;
+        }
+        cp_commit();
+    };
+    load_rows(0);                                       // on their way while the keys are made operands
     int row[4];                                         // pool rows of keys j0 + g + 8 i, -1: none
     uint32_t a[2][D / 16][4];
     const int kgrp = t * (D / 4) / GS;
@@ -532,25 +602,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
             a[i / 2][2 * w + 1][2 + i % 2] = pr[w][3];
         }
     }
-    // rows of the tokens that see any of the block's keys
-    const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
-    const int tiles = (row_end - row_lo + QR - 1) / QR;
-    auto load_rows = [&](int s) {
-        for (int i = tid; i < QR * (D / 8); i += 128) {
-            const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
-            const bool ok = r < row_end;
-            const int tok = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
-            cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
-        }
-        if (tid < QR) {
-            const int r = row_lo + s * QR + tid;
-            const int tok = r / plan.share, h = head * plan.share + r % plan.share;
-            sl[s & 1][tid] = r < row_end ? __ldg(lse + static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h) * kLog2e : INFINITY;
-        }
-        cp_commit();
-    };
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    load_rows(0);
     for (int s = 0; s < tiles; ++s) {
         if (s + 1 < tiles)
             load_rows(s + 1);
@@ -603,8 +655,8 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
 
 struct AttnPlan {
     int share, row_tile, target, slots;
-    int64_t units, records_bytes, parts_bytes, lse_bytes;
-    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes; }
+    int64_t units, records_bytes, parts_bytes, lse_bytes, fresh_bytes, score_bytes;
+    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes + fresh_bytes + score_bytes; }
 };
 
 inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -615,13 +667,16 @@ AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total,
     const int64_t rows = static_cast<int64_t>(most) * p.share;
     p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
     // units times heads wanted: what the device holds at once
-    p.target = p.row_tile <= 16 ? rows_warps(c->head_dim, p.row_tile) * sm_count() : paged_tile_target(p.row_tile, c->head_dim);
+    p.target = p.row_tile <= 16 ? rows_warps(c->head_dim, p.row_tile) * sm_count() : paged_tile_target(p.row_tile);
     // every sequence's row tiles, and what their parts add (the bounds stand at find_unit)
     const int64_t more = (p.target + c->n_kv_heads - 1) / c->n_kv_heads;
     p.units = (static_cast<int64_t>(total) * p.share) / p.row_tile + batch + more;
     p.slots = static_cast<int>(2 * more);
     p.records_bytes = 256 + up256(static_cast<int64_t>(p.slots) * sizeof(SplitRecord));
     p.parts_bytes = up256(static_cast<int64_t>(p.slots) * c->n_kv_heads * p.row_tile * (c->head_dim + 4) * 4);
+    const bool one = accumulate && rows == 1;
+    p.fresh_bytes = one ? up256(static_cast<int64_t>(batch) * n_heads * 4) : 0;
+    p.score_bytes = one ? up256(static_cast<int64_t>(c->num_pages) * c->page_size * c->n_kv_heads * 4) : 0;
     p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
     return p;
 }
@@ -691,6 +746,11 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     a.parts = reinterpret_cast<float*>(w + p.records_bytes);
     a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes) : lse;
     a.slots = p.slots;
+    if (p.score_bytes > 0) {
+        w += p.records_bytes + p.parts_bytes + p.lse_bytes;
+        a.fresh = reinterpret_cast<float*>(w);
+        a.scores = reinterpret_cast<float*>(w + p.fresh_bytes);
+    }
     const cudaStream_t st = as_stream(stream);
     const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;
     if (p.row_tile > 16) {
@@ -718,7 +778,10 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
 #undef ROWS_N
 #undef ROWS
     }
-    if (accumulate) {
+    if (a.scores != nullptr) {
+        const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
+        launch_k(paged_weight_one_kernel, dim3(static_cast<unsigned>((cap + (k_new ? 1 : 0) + 511) / 512), kvh, batch), dim3(128), 0, st, true, a);
+    } else if (accumulate) {
         const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
         // every 128 slots, and 128 fresh tokens; blocks behind a sequence's end return at once
         const dim3 wgrid(static_cast<unsigned>((cap + 127) / 128 + (k_new ? (most + 127) / 128 : 0)), kvh, batch);

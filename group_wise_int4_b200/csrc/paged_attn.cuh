@@ -138,41 +138,50 @@ struct Unit {
 };
 
 // MIN: blocks of keys that a part has at least; less costs more to join than it saves.
-template <int R, int KEYS, int MIN>
+// FULL: where the tiles alone take more than half of the target, parts are as long as FULL
+// times an even share of the work: short enough to level the blocks' ends, and 1 or 2 by
+// what starting and joining a part costs beside its keys.
+template <int R, int KEYS, int MIN, int FULL>
 __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
     const int lane = threadIdx.x & 31;
+    struct Seq {
+        int n, ctx, first, tiles;
+    };
+    auto load = [&](int b) {
+        Seq s{};
+        if (b < p.batch) {
+            s.n = rows_of(rows, b, s.first, c.status);
+            s.ctx = slots_of(c, b);
+            s.tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.share + R - 1) / R);
+        }
+        return s;
+    };
     // work of the whole batch, in key blocks times row tiles, and the row tiles
+    Seq q = load(lane);                                 // a batch of up to 32 is read once
     int64_t work = 0, all = 0;
-    for (int b = lane; b < p.batch; b += 32) {
-        int first;
-        const int n = rows_of(rows, b, first, c.status);
-        const int64_t tiles = (static_cast<int64_t>(n) * p.share + R - 1) / R;
-        work += tiles * ((slots_of(c, b) + KEYS - 1) / KEYS);
-        all += tiles;
+    for (int b = lane;; b += 32) {
+        const Seq s = b < 32 ? q : load(b);
+        work += static_cast<int64_t>(s.tiles) * ((s.ctx + KEYS - 1) / KEYS);
+        all += s.tiles;
+        if (b - lane + 32 >= p.batch) break;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         work += __shfl_xor_sync(0xffffffffu, work, o);
         all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    // With room for every tile's first part beside them the parts fit the target: they run at
-    // once. Many tiles need no such care.
-    const int64_t fit = p.target - all * p.heads, room = fit > p.target / 2 ? fit : p.target;
+    // With room for every tile's first part beside them the parts fit the target: they run at once.
+    const int64_t fit = p.target - all * p.heads;
+    const int64_t room = fit > p.target / 2 ? fit : (p.target + FULL - 1) / FULL;
     const int64_t even = (work * p.heads + room - 1) / room;
     Unit u{};
     u.plan_per = static_cast<int>(even < MIN ? MIN : even > (1 << 30) ? (1 << 30) : even);
     int64_t before = 0, split = 0;                      // units, and units of split tiles, of the sequences passed
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        int n = 0, ctx = 0, first = 0, tiles = 0, parts = 0;
-        if (b < p.batch) {
-            n = rows_of(rows, b, first, c.status);
-            ctx = slots_of(c, b);
-            tiles = static_cast<int>((static_cast<int64_t>(n) * p.share + R - 1) / R);
-            parts = max(1, ((ctx + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per);
-        }
+        if (b0 > 0) q = load(b0 + lane);
+        const int parts = max(1, ((q.ctx + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per);
         // (more units than 2^25 of one sequence would be more than a launch has)
-        const int mine = static_cast<int>(min(static_cast<int64_t>(tiles) * parts, static_cast<int64_t>(1 << 25)));
+        const int mine = static_cast<int>(min(static_cast<int64_t>(q.tiles) * parts, static_cast<int64_t>(1 << 25)));
         const int mine2 = parts > 1 ? mine : 0;
         const int sum = __reduce_add_sync(0xffffffffu, mine), sum2 = __reduce_add_sync(0xffffffffu, mine2);
         if (unit >= before + sum) {
@@ -193,9 +202,9 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
         const int l = __ffs(__ballot_sync(0xffffffffu, want < x)) - 1;
         const int at = want - __shfl_sync(0xffffffffu, x - mine, l);
         u.b = b0 + l;
-        u.n = __shfl_sync(0xffffffffu, n, l);
-        u.ctx = __shfl_sync(0xffffffffu, ctx, l);
-        u.first = __shfl_sync(0xffffffffu, first, l);
+        u.n = __shfl_sync(0xffffffffu, q.n, l);
+        u.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
+        u.first = __shfl_sync(0xffffffffu, q.first, l);
         u.parts = __shfl_sync(0xffffffffu, parts, l);
         u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
         u.slot = static_cast<int>(split) + __shfl_sync(0xffffffffu, y - mine2, l) + at;
@@ -225,6 +234,8 @@ struct AttnArgs {
     __half* o;
     float* lse;
     float* parts;
+    float *scores, *fresh;      // one row a sequence and key head, weights wanted: its scores, by slot's row and
+                                // of its own token [batch][heads]; else nullptr
     int* split_units;           // how many partial slots are in use
     SplitRecord* records;       // [slots]
     int slots;                  // of partial results
@@ -341,7 +352,7 @@ void launch_join(const AttnArgs& a, cudaStream_t st) {
 
 // The tcgen05 kernel over tiles of paged_tile_rows() query rows; `units` blocks per key head.
 int paged_tile_rows(int rows);
-int paged_tile_target(int row_tile, int head_dim);
+int paged_tile_target(int row_tile);
 void launch_paged_tile(const AttnArgs& a, int head_dim, int bits, int group, int row_tile, int64_t units, cudaStream_t st);
 
 }  // namespace flexq

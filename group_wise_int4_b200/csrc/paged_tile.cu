@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     pdl_wait();
     pdl_trigger();
     const int head = blockIdx.x % A.plan.heads;
-    const Unit u = find_unit<R, 128, kTileMin>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
+    const Unit u = find_unit<R, 128, kTileMin, 2>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
     if (warp == 0) record_split<R, 128>(A, u, blockIdx.x / A.plan.heads, head);
     if (!u.live) return;
     const int share = A.plan.share;
@@ -470,8 +470,8 @@ void launch_one(const AttnArgs& a, int64_t units, cudaStream_t st) {
 // Rows of a sequence and key head -> rows of a tile.
 int paged_tile_rows(int rows) { return rows <= 128 ? 128 : 256; }
 
-// Blocks wanted: a few for every one that the device holds at once.
-int paged_tile_target(int row_tile, int) { return sm_count() * (row_tile == 128 ? 2 : 1) * 2; }
+// Blocks that the device holds at once.
+int paged_tile_target(int row_tile) { return sm_count() * (row_tile == 128 ? 2 : 1); }
 
 void launch_paged_tile(const AttnArgs& a, int head_dim, int bits, int group, int row_tile, int64_t units, cudaStream_t st) {
 #define TILE(D_, B_, G_) row_tile == 128 ? launch_one<D_, B_, G_, 1>(a, units, st) : launch_one<D_, B_, G_, 2>(a, units, st)
