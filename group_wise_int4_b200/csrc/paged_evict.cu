@@ -8,6 +8,12 @@
 // moves a few slots instead of shifting half of the cache, which is why a slot's position
 // is stored beside it and its order in the cache means nothing to attention.
 //
+// Tables of up to 2048 slots: one launch, a block per (sequence, head) that holds 8
+// consecutive slots a thread (one page lookup, two wide loads each of weights and positions),
+// finds the budget-th largest key bit by bit with counts over the block, lists the moves
+// with two block scans and copies. Nothing passes through memory but what has to; latency
+// bounds it. Longer tables: select and move below.
+//
 // select: one block per (sequence, head). The keys (an order-preserving integer of the
 // weight, the largest value for the recent slots) go to shared memory once, the
 // budget-th largest is found digit by digit from histograms (11 + 11 + 10 bits), and one
@@ -30,6 +36,170 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) u = 0xFF800000u;
     if (u == 0x80000000u) u = 0u;
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int PS_T = 256, PS_PER = 8, PS_SLOTS = PS_T * PS_PER;      // threads, slots a thread, slots at most
+
+// U: moves that 8 lanes have under way at once; few of them leave registers for more blocks.
+template <int KB, int U>
+__global__ void __launch_bounds__(PS_T, U == 1 ? 7 : 4) evict_small_kernel(PagedView c, int budget, int recent, int ng,
+                                                              int32_t* __restrict__ new_len) {
+    constexpr int WARPS = PS_T / 32, PL = KB >= 64 ? KB / 64 : 1;    // 16-byte pieces of a lane: keys', then values'
+    __shared__ int pages[PS_SLOTS / 16];
+    __shared__ uint16_t from[PS_SLOTS / 2], to[PS_SLOTS / 2];        // moves: at most half of the slots
+    __shared__ int red[2][WARPS], moved_count;
+    pdl_wait();
+    pdl_trigger();
+    const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = slots_of(c, b);
+    if (head == 0 && tid == 0) new_len[b] = min(n, budget);
+    if (n <= budget) return;
+    for (int i = tid; i < (n + (1 << c.shift) - 1) >> c.shift; i += PS_T) pages[i] = page_of(c, b, i << c.shift);
+    __syncthreads();
+    // warps without a slot wait for the moves; the others meet at a barrier of their own
+    const int active = (n + 32 * PS_PER - 1) / (32 * PS_PER);
+    auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"r"(active * 32) : "memory"); };
+    int total = 0;
+    if (warp < active) {
+        const int j0 = tid * PS_PER;                                     // 8 slots lie in one page
+        const int page = j0 < n ? pages[j0 >> c.shift] : -1;
+        const int64_t row = page < 0 ? 0 : slot_row(c, page, head, j0);
+        // a slot behind a bad page id counts as the oldest, with no weight, and never moves
+        uint32_t key[PS_PER];
+        {
+            int pos[PS_PER];
+            float w[PS_PER];
+#pragma unroll
+            for (int i = 0; i < PS_PER; i += 4) {
+                const int4 p4 = page < 0 ? make_int4(0, 0, 0, 0) : *reinterpret_cast<const int4*>(c.slot_pos + row + i);
+                const float4 w4 = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(c.weight + row + i);
+                pos[i] = p4.x, pos[i + 1] = p4.y, pos[i + 2] = p4.z, pos[i + 3] = p4.w;
+                w[i] = w4.x, w[i + 1] = w4.y, w[i + 2] = w4.z, w[i + 3] = w4.w;
+            }
+            int latest = INT32_MIN;
+#pragma unroll
+            for (int i = 0; i < PS_PER; ++i)
+                if (page >= 0 && j0 + i < n) latest = max(latest, pos[i]);
+            latest = __reduce_max_sync(0xffffffffu, latest);
+            if (lane == 0) red[0][warp] = latest;
+            meet();
+            for (int i = 0; i < active; ++i) latest = max(latest, red[0][i]);
+            const int64_t after = static_cast<int64_t>(latest) - recent;
+#pragma unroll
+            for (int i = 0; i < PS_PER; ++i)
+                key[i] = page < 0 || j0 + i >= n ? 0u : pos[i] > after ? 0xFFFFFFFFu : weight_key(w[i]);
+        }
+        // the budget-th largest key: the largest T with at least `budget` keys >= T. Where exactly that
+        // many are, they are the kept ones and the search is over.
+        uint32_t T = 0;
+        int need = 0;                                                    // of the keys equal to T; 0: not known yet
+        int side = 1, above = 0;
+        auto count = [&](uint32_t bound) {                               // keys >= bound, of the block
+            int v = 0;
+#pragma unroll
+            for (int i = 0; i < PS_PER; ++i) v += key[i] >= bound;
+            v = __reduce_add_sync(0xffffffffu, v);
+            if (lane == 0) red[side][warp] = v;
+            meet();
+            v = __reduce_add_sync(0xffffffffu, lane < active ? red[side][lane] : 0);
+            side ^= 1;
+            return v;
+        };
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t bound = T | (1u << bit);
+            const int v = count(bound);
+            if (v >= budget) T = bound;
+            if (v == budget) {
+                need = PS_SLOTS;
+                break;
+            }
+            if (v < budget) above = v;                                   // in the end: the keys > T
+        }
+        if (need == 0) need = budget - above;
+        // kept: keys above T, and the first `need` of those equal to it
+        auto scan = [&](int v, int& total) {                             // exclusive prefix over the block
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) red[side][warp] = x;
+            meet();
+            const int other = lane < active ? red[side][lane] : 0;
+            total = __reduce_add_sync(0xffffffffu, other);
+            side ^= 1;
+            return __reduce_add_sync(0xffffffffu, lane < warp ? other : 0) + x - v;
+        };
+        int ties = 0;
+#pragma unroll
+        for (int i = 0; i < PS_PER; ++i) ties += j0 + i < n && key[i] == T;
+        int rank = scan(ties, total);
+        int keep = 0, moves = 0;                                         // bits: kept; counts: holes, moved << 16
+#pragma unroll
+        for (int i = 0; i < PS_PER; ++i) {
+            if (j0 + i >= n) continue;
+            const bool tie = key[i] == T, k = key[i] > T || (tie && rank < need);
+            rank += tie;
+            keep |= k << i;
+            if (j0 + i < budget) moves += !k;
+            else moves += k << 16;
+        }
+        int at = scan(moves, total);
+#pragma unroll
+        for (int i = 0; i < PS_PER; ++i) {
+            if (j0 + i >= n) continue;
+            const bool k = keep >> i & 1;
+            if (j0 + i < budget) {
+                if (!k) to[at++ & 0xFFFF] = static_cast<uint16_t>(j0 + i);
+            } else if (k) {
+                from[at >> 16] = static_cast<uint16_t>(j0 + i);
+                at += 1 << 16;
+            }
+        }
+        if (tid == 0) moved_count = total & 0xFFFF;
+    }
+    __syncthreads();
+    // 8 lanes a move, U moves at once. No slot is both read and written: what is given up lies
+    // below the budget, what moves behind it.
+    const int moved = moved_count, l = tid & 7;
+    for (int i0 = tid >> 3; i0 < moved; i0 += U * (PS_T / 8)) {
+        uint4 x[U][PL];
+        uint32_t meta[U], other[U];
+        int64_t dst[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * (PS_T / 8);
+            dst[u] = -1;
+            if (i >= moved) continue;
+            const int sj = from[i], dj = to[i], sp = pages[sj >> c.shift], dp = pages[dj >> c.shift];
+            if (sp < 0 || dp < 0) continue;
+            const int64_t s = slot_row(c, sp, head, sj);
+            dst[u] = slot_row(c, dp, head, dj);
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                const int piece = l + k * 8;
+                if (piece < KB / 8)
+                    x[u][k] = *reinterpret_cast<const uint4*>((piece < KB / 16 ? c.kc : c.vc) + s * KB + piece % (KB / 16) * 16);
+            }
+            if (l < 2 * ng) meta[u] = (l < ng ? c.km : c.vm)[s * ng + (l < ng ? l : l - ng)];
+            if (l == 6) other[u] = __float_as_uint(c.weight[s]);
+            if (l == 7) other[u] = static_cast<uint32_t>(c.slot_pos[s]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (dst[u] < 0) continue;
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                const int piece = l + k * 8;
+                if (piece < KB / 8)
+                    *reinterpret_cast<uint4*>((piece < KB / 16 ? c.kc : c.vc) + dst[u] * KB + piece % (KB / 16) * 16) = x[u][k];
+            }
+            if (l < 2 * ng) (l < ng ? c.km : c.vm)[dst[u] * ng + (l < ng ? l : l - ng)] = meta[u];
+            if (l == 6) c.weight[dst[u]] = __uint_as_float(other[u]);
+            if (l == 7) c.slot_pos[dst[u]] = static_cast<int32_t>(other[u]);
+        }
+    }
 }
 
 // Workspace of one (sequence, head): the number of moves, then from[] and to[].
@@ -245,6 +415,19 @@ extern "C" int flex_paged_evict(const flex_paged_cache* cache, int32_t budget, i
     const cudaStream_t st = as_stream(stream);
     const int most = static_cast<int>(evict_most(cache, budget));
     const int cap = cache->max_pages * cache->page_size;
+    if (cap <= PS_SLOTS) {
+        const int kb = cache->head_dim * cache->cfg.num_bits / 8, ng = cache->head_dim / cache->cfg.group_size;
+        const dim3 grid(cache->n_kv_heads, cache->batch);
+#define SMALL(KB_, U_) launch_k(evict_small_kernel<KB_, U_>, grid, dim3(PS_T), 0, st, true, view, budget, recent, ng, new_len)
+        // up to 64 moves a head (a cache a few tokens over its budget) are two rounds of one move a lane group
+        if (most <= 64) {
+            if (kb == 32) SMALL(32, 1); else if (kb == 64) SMALL(64, 1); else SMALL(128, 1);
+        } else {
+            if (kb == 32) SMALL(32, 4); else if (kb == 64) SMALL(64, 4); else SMALL(128, 4);
+        }
+#undef SMALL
+        return launch_status();
+    }
     const int cached = cap < PE_CACHE ? cap : PE_CACHE;
     const int smem = (cached + PE_BINS) * 4;
     set_smem_once(evict_select_kernel, (PE_CACHE + PE_BINS) * 4);
