@@ -2,10 +2,12 @@
 //
 // store: q = the codec's quantiser (quant.cuh) of the new rows, into the slots behind
 // ctx_len; load: the codec's value of a run of slots, into rows. Both are a stream: every
-// value is read once and written once, so HBM bounds them. A thread owns 8 values (16
-// bytes of fp16, 4 or 8 bytes of codes); a block's threads lie along a token's row (heads,
-// then dims), so rows are read and written in whole lines and each head's slot is one
-// 32- to 128-byte piece. TOKENS tokens a thread keep that many loads in flight.
+// value is read once and written once, so HBM bounds them as long as the instructions are
+// few: a thread owns 16 values (32 bytes of fp16, 8 or 16 bytes of codes), so that a
+// group's extremes, scale and step are worked out by few lanes, and TOKENS tokens, whose
+// rows it requests first and whose slots lie in two pages at most. A block's threads lie
+// along a token's row (heads, then dims): rows are read and written in whole lines, each
+// head's slot in one piece of 32 to 128 bytes.
 #include "paged.cuh"
 
 namespace flexq {
@@ -13,11 +15,32 @@ namespace {
 
 constexpr int PS_THREADS = 256;
 
-template <int BITS, int GS, int TOKENS>
+// The pages of TOKENS slots from `slot` on: the first one's and the last one's.
+template <int TOKENS>
+struct SlotRows {
+    int entry0, entry1, base;
+    __device__ __forceinline__ SlotRows(const PagedView& c, int b, int64_t slot, int count) {
+        const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_pages;
+        const int cap = paged_capacity(c);
+        const int64_t end = slot + count - 1;
+        base = slot < 0 || slot >= cap ? INT32_MIN : static_cast<int>(slot);
+        entry0 = page_entry(c, row, base, base != INT32_MIN);
+        entry1 = TOKENS == 1 ? entry0 : page_entry(c, row, static_cast<int>(end), end >= 0 && end < cap);
+        if (base == INT32_MIN || end >= cap) paged_bad(c);
+    }
+    // row of the i-th slot and this head; -1 where it lies outside the table or its page outside the pool
+    __device__ __forceinline__ int row(const PagedView& c, int head, int i) const {
+        if (base == INT32_MIN || base + i >= paged_capacity(c)) return -1;
+        const int slot = base + i;
+        return entry_row(c, (slot >> c.shift) == (base >> c.shift) ? entry0 : entry1, head, slot);
+    }
+};
+
+template <int D, int BITS, int GS, int TOKENS>
 __global__ void __launch_bounds__(PS_THREADS) paged_store_kernel(PagedView c, RowsOf rows, const __half* __restrict__ k_new,
                                                                  const __half* __restrict__ v_new, int64_t row_stride,
-                                                                 const int32_t* __restrict__ pos0, int dim) {
-    constexpr int L = GS / 8;                       // lanes of a group
+                                                                 const int32_t* __restrict__ pos0) {
+    constexpr int L = GS / 16, V = D / 16, KB = D * BITS / 8, NG = D / GS;      // lanes of a group, threads of a head
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.z;
@@ -25,53 +48,56 @@ __global__ void __launch_bounds__(PS_THREADS) paged_store_kernel(PagedView c, Ro
     const int n = rows_of(rows, b, first, c.status);
     const int t0 = blockIdx.x * TOKENS;
     if (t0 >= n) return;
-    const int vecs = c.heads * dim / 8;             // vectors of one row
+    const int vecs = c.heads * V;                   // threads of one row's keys
     const int col = blockIdx.y * PS_THREADS + threadIdx.x;
     const bool live = col < 2 * vecs;               // keys, then values
-    const int which = live && col >= vecs;
-    const int e = live ? (col - which * vecs) * 8 : 0;
-    const int head = e / dim, d = e % dim;
-    const __half* src = (which ? v_new : k_new) + e;
-    uint4 v[TOKENS];
+    const int which = live && col >= vecs, e = live ? col - which * vecs : 0, head = e / V, d = e % V * 16;
+    const __half* src = (which ? v_new : k_new) + static_cast<int64_t>(first + t0) * row_stride + e * 16;
+    const int count = min(TOKENS, n - t0);
+    uint4 v[TOKENS][2];
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (live && t0 + i < n) v[i] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(first + t0 + i) * row_stride);
+        v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+        if (live && i < count) {
+            const uint4* p = reinterpret_cast<const uint4*>(src + i * row_stride);
+            v[i][0] = ld_stream_v4(p);
+            v[i][1] = ld_stream_v4(p + 1);
+        }
     }
-    const int ctx = slots_of(c, b), cap = paged_capacity(c);
+    const int ctx = slots_of(c, b);
     const int start = pos0 ? __ldg(pos0 + b) : ctx;
-    const int kb = dim * BITS / 8, ng = dim / GS;
+    const SlotRows<TOKENS> slots(c, b, static_cast<int64_t>(ctx) + t0, count);
+    uint8_t* const codes = (which ? c.vc : c.kc) + d * BITS / 8;
+    uint32_t* const meta = (which ? c.vm : c.km) + d / GS;
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
-        __half2 hmn, hmx;
+        __half2 hmn, hmx, hmn1, hmx1;
         float mn, mx;
-        minmax8(v[i], hmn, hmx);
-        group_minmax<L>(hmn, hmx, mn, mx);
+        minmax8(v[i][0], hmn, hmx);
+        minmax8(v[i][1], hmn1, hmx1);
+        group_minmax<L>(__hmin2(hmn, hmn1), __hmax2(hmx, hmx1), mn, mx);
         const __half s16 = group_scale16<BITS>(mn, mx);
         const float s = __half2float(s16);
-        if (!live || t0 + i >= n) continue;
-        const int slot = ctx + t0 + i;
-        if (slot >= cap) {
-            paged_bad(c);
-            continue;
+        if (!live || i >= count) continue;
+        const int row = slots.row(c, head, i);
+        if (row < 0) continue;
+        uint8_t* const to = codes + static_cast<int64_t>(row) * KB;
+        if (BITS == 4) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(quant8_4bit(v[i][0], mn, s), quant8_4bit(v[i][1], mn, s));
+        } else {
+            const uint2 a = quant8_8bit(v[i][0], mn, s), z = quant8_8bit(v[i][1], mn, s);
+            *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, z.x, z.y);
         }
-        const int page = page_of(c, b, slot);
-        if (page < 0) continue;
-        const int64_t row = slot_row(c, page, head, slot);
-        uint8_t* codes = (which ? c.vc : c.kc) + row * kb + d * BITS / 8;
-        if (BITS == 4)
-            *reinterpret_cast<uint32_t*>(codes) = quant8_4bit(v[i], mn, s);
-        else
-            *reinterpret_cast<uint2*>(codes) = quant8_8bit(v[i], mn, s);
-        if (d % GS == 0) (which ? c.vm : c.km)[row * ng + d / GS] = pack_half2_bits(stored_min16(mn), s16);
+        if (d % GS == 0) meta[static_cast<int64_t>(row) * NG] = pack_half2_bits(stored_min16(mn), s16);
         if (c.slot_pos && !which && d == 0) c.slot_pos[row] = start + t0 + i;
     }
 }
 
-template <int BITS, int GS, int TOKENS>
+template <int D, int BITS, int GS, int TOKENS>
 __global__ void __launch_bounds__(PS_THREADS) paged_load_kernel(PagedView c, RowsOf rows, __half* __restrict__ k_out,
                                                                 __half* __restrict__ v_out, int64_t row_stride,
-                                                                const int32_t* __restrict__ from, int dim) {
+                                                                const int32_t* __restrict__ from) {
+    constexpr int V = D / 16, KB = D * BITS / 8, NG = D / GS;
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.z;
@@ -79,56 +105,55 @@ __global__ void __launch_bounds__(PS_THREADS) paged_load_kernel(PagedView c, Row
     const int n = rows_of(rows, b, first, c.status);
     const int t0 = blockIdx.x * TOKENS;
     if (t0 >= n) return;
-    const int vecs = c.heads * dim / 8;
+    const int vecs = c.heads * V;
     const int col = blockIdx.y * PS_THREADS + threadIdx.x;
     if (col >= 2 * vecs) return;
-    const int which = col >= vecs;
-    const int e = (col - which * vecs) * 8;
-    const int head = e / dim, d = e % dim;
-    const int start = from ? __ldg(from + b) : 0, cap = paged_capacity(c);
-    const int kb = dim * BITS / 8, ng = dim / GS;
-    uint2 q[TOKENS];
+    const int which = col >= vecs, e = col - which * vecs, head = e / V, d = e % V * 16;
+    const int count = min(TOKENS, n - t0);
+    const SlotRows<TOKENS> slots(c, b, static_cast<int64_t>(from ? __ldg(from + b) : 0) + t0, count);
+    const uint8_t* const codes = (which ? c.vc : c.kc) + d * BITS / 8;
+    const uint32_t* const metas = (which ? c.vm : c.km) + d / GS;
+    uint4 q[TOKENS];
     uint32_t meta[TOKENS];
-    int64_t row[TOKENS];
+    bool ok[TOKENS];
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
-        row[i] = -1;
-        if (t0 + i >= n) continue;
-        const int64_t slot = static_cast<int64_t>(start) + t0 + i;
-        if (slot < 0 || slot >= cap) {
-            paged_bad(c);
-            continue;
+        const int row = i < count ? slots.row(c, head, i) : -1;
+        ok[i] = row >= 0;
+        if (row < 0) continue;
+        const uint8_t* at = codes + static_cast<int64_t>(row) * KB;
+        if (BITS == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
+            q[i] = make_uint4(x.x, x.y, 0u, 0u);
+        } else {
+            q[i] = *reinterpret_cast<const uint4*>(at);
         }
-        const int page = page_of(c, b, static_cast<int>(slot));
-        if (page >= 0) row[i] = slot_row(c, page, head, static_cast<int>(slot));
+        meta[i] = metas[static_cast<int64_t>(row) * NG];
     }
+    __half* const dst = (which ? v_out : k_out) + static_cast<int64_t>(first + t0) * row_stride + e * 16;
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) {
-        if (row[i] < 0) continue;
-        const uint8_t* codes = (which ? c.vc : c.kc) + row[i] * kb + d * BITS / 8;
-        q[i] = BITS == 4 ? make_uint2(*reinterpret_cast<const uint32_t*>(codes), 0u) : *reinterpret_cast<const uint2*>(codes);
-        meta[i] = (which ? c.vm : c.km)[row[i] * ng + d / GS];
-    }
-#pragma unroll
-    for (int i = 0; i < TOKENS; ++i) {
-        if (row[i] < 0) continue;
+        if (!ok[i]) continue;
+        // a constant group: step 0 and codes 0 give min
         const float mn = h2f_lo(meta[i]), step = group_step(__ushort_as_half(static_cast<unsigned short>(meta[i] >> 16)));
-        uint32_t w[4];
+        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {                  // values 2k and 2k + 1
             uint32_t a, z;
             if (BITS == 4) {
-                a = (q[i].x >> (8 * k)) & 15u;
-                z = (q[i].x >> (8 * k + 4)) & 15u;
+                const uint32_t x = (k < 4 ? q[i].x : q[i].y) >> (8 * (k & 3));
+                a = x & 15u;
+                z = (x >> 4) & 15u;
             } else {
-                const uint32_t x = k < 2 ? q[i].x : q[i].y;
-                a = (x >> (16 * (k & 1))) & 255u;
-                z = (x >> (16 * (k & 1) + 8)) & 255u;
+                const uint32_t x = (k < 2 ? q[i].x : k < 4 ? q[i].y : k < 6 ? q[i].z : q[i].w) >> (16 * (k & 1));
+                a = x & 255u;
+                z = (x >> 8) & 255u;
             }
-            w[k] = dequant_two(a, z, step, mn);     // a constant group: step 0 and codes 0 give min
+            w[k] = dequant_two(a, z, step, mn);
         }
-        __half* dst = (which ? v_out : k_out) + static_cast<int64_t>(first + t0 + i) * row_stride + e;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        uint4* to = reinterpret_cast<uint4*>(dst + i * row_stride);
+        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
@@ -195,7 +220,7 @@ int validate_kv_rows(const flex_paged_cache* c, const void* k, const void* v, in
 }
 
 inline dim3 paged_copy_grid(const flex_paged_cache* c, int batch, int most, int tokens) {
-    const int64_t vecs = 2LL * c->n_kv_heads * c->head_dim / 8;
+    const int64_t vecs = 2LL * c->n_kv_heads * c->head_dim / 16;
     return dim3((most + tokens - 1) / tokens, static_cast<unsigned>((vecs + PS_THREADS - 1) / PS_THREADS), batch);
 }
 
@@ -205,24 +230,28 @@ inline dim3 paged_copy_grid(const flex_paged_cache* c, int batch, int most, int 
 using namespace flexq;
 
 // One token a thread where there is one (a decode step), four otherwise.
-#define PAGED_COPY(KERNEL, ...)                                                                                   \
-    do {                                                                                                          \
-        const int B = cache->cfg.num_bits, G = cache->cfg.group_size;                                             \
-        const cudaStream_t st = as_stream(stream);                                                                \
-        if (most == 1) {                                                                                          \
-            const dim3 grid = paged_copy_grid(cache, batch, most, 1);                                             \
-            if (B == 4 && G == 32) launch_k(KERNEL<4, 32, 1>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);  \
-            else if (B == 4) launch_k(KERNEL<4, 64, 1>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);        \
-            else if (G == 32) launch_k(KERNEL<8, 32, 1>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);       \
-            else launch_k(KERNEL<8, 64, 1>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);                    \
-        } else {                                                                                                  \
-            const dim3 grid = paged_copy_grid(cache, batch, most, 4);                                             \
-            if (B == 4 && G == 32) launch_k(KERNEL<4, 32, 4>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);  \
-            else if (B == 4) launch_k(KERNEL<4, 64, 4>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);        \
-            else if (G == 32) launch_k(KERNEL<8, 32, 4>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);       \
-            else launch_k(KERNEL<8, 64, 4>, grid, dim3(PS_THREADS), 0, st, true, __VA_ARGS__);                    \
-        }                                                                                                         \
-        return launch_status();                                                                                   \
+#define PAGED_COPY(KERNEL, ...)                                                                                     \
+    do {                                                                                                            \
+        const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;                          \
+        const cudaStream_t st = as_stream(stream);                                                                  \
+        const dim3 grid = paged_copy_grid(cache, batch, most, most == 1 ? 1 : 4), block(PS_THREADS);                \
+        if (D == 64) {                                                                                              \
+            if (B == 4 && G == 32) PAGED_RUN(KERNEL, 64, 4, 32, __VA_ARGS__);                                       \
+            else if (B == 4) PAGED_RUN(KERNEL, 64, 4, 64, __VA_ARGS__);                                             \
+            else if (G == 32) PAGED_RUN(KERNEL, 64, 8, 32, __VA_ARGS__);                                            \
+            else PAGED_RUN(KERNEL, 64, 8, 64, __VA_ARGS__);                                                         \
+        } else {                                                                                                    \
+            if (B == 4 && G == 32) PAGED_RUN(KERNEL, 128, 4, 32, __VA_ARGS__);                                      \
+            else if (B == 4) PAGED_RUN(KERNEL, 128, 4, 64, __VA_ARGS__);                                            \
+            else if (G == 32) PAGED_RUN(KERNEL, 128, 8, 32, __VA_ARGS__);                                           \
+            else PAGED_RUN(KERNEL, 128, 8, 64, __VA_ARGS__);                                                        \
+        }                                                                                                           \
+        return launch_status();                                                                                     \
+    } while (0)
+#define PAGED_RUN(KERNEL, D_, B_, G_, ...)                                            \
+    do {                                                                              \
+        if (most == 1) launch_k(KERNEL<D_, B_, G_, 1>, grid, block, 0, st, true, __VA_ARGS__); \
+        else launch_k(KERNEL<D_, B_, G_, 4>, grid, block, 0, st, true, __VA_ARGS__);  \
     } while (0)
 
 extern "C" int flex_paged_store_kv(const flex_paged_cache* cache, const void* k_new, const void* v_new, int64_t row_stride,
@@ -236,7 +265,7 @@ extern "C" int flex_paged_store_kv(const flex_paged_cache* cache, const void* k_
     if (most == 0 || total == 0) return FLEX_OK;
     const PagedView view = paged_view(cache);
     PAGED_COPY(paged_store_kernel, view, (RowsOf{cu_new, most, total}), static_cast<const __half*>(k_new),
-               static_cast<const __half*>(v_new), row_stride, pos0, cache->head_dim);
+               static_cast<const __half*>(v_new), row_stride, pos0);
 }
 
 extern "C" int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, void* v_out, int64_t row_stride,
@@ -250,5 +279,5 @@ extern "C" int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, vo
     if (most == 0 || total == 0) return FLEX_OK;
     const PagedView view = paged_view(cache);
     PAGED_COPY(paged_load_kernel, view, (RowsOf{cu_rows, most, total}), static_cast<__half*>(k_out),
-               static_cast<__half*>(v_out), row_stride, start, cache->head_dim);
+               static_cast<__half*>(v_out), row_stride, start);
 }
