@@ -9,7 +9,6 @@ are not given are allocated with torch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -557,86 +556,91 @@ def _need(t, dtype, device, name, shape=None):
         raise ValueError(f"{name}: a contiguous tensor of shape {shape} expected, got {tuple(t.shape)}")
 
 
-def _need_rows(t, dtype, device, name, total, stride, width):
-    """Rows of `stride` elements, the first `width` of which are used, lie within the tensor's memory."""
-    if t.dtype != dtype or t.device != device:
+def _need_rows(t, dtype, size, device, name, total, stride, width):
+    """Rows of `stride` elements (of `size` bytes), the first `width` of which are used, lie within
+    the tensor's memory."""
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
-    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-    if total and (stride < width or (total - 1) * stride + width > have):
-        raise ValueError(f"{name}: {total} rows of {stride} elements expected, {have} elements are there")
+    if total and (stride < width or
+                  (t.storage_offset() + (total - 1) * stride + width) * size > t.untyped_storage().nbytes()):
+        raise ValueError(f"{name}: {total} rows of {stride} elements expected, "
+                         f"{t.untyped_storage().nbytes() // size - t.storage_offset()} elements are there")
 
 
 def _rows_call(cache, cu, most, total, batch):
-    """(batch, total) of a ragged call, checked against cu's length."""
+    """(batch, total, address of cu) of a ragged call, checked against cu's length."""
     if cu is None:
         batch = cache.batch if batch is None else int(batch)
-        total = batch * int(most)
-    else:
+        return batch, batch * int(most), None
+    if cu.dtype is not torch.int32 or cu.device != cache.device or cu.dim() != 1 or not cu.is_contiguous():
         _need(cu, torch.int32, cache.device, "cu", (None,))
-        batch = cu.shape[0] - 1 if batch is None else int(batch)
-        if cu.shape[0] < batch + 1:
-            raise ValueError(f"cu: {batch + 1} offsets expected, got {cu.shape[0]}")
-        if total is None:
-            raise ValueError("total: the number of rows that cu may reach is needed with cu")
-    return batch, int(total)
+    n = cu.numel()
+    if batch is None:
+        batch = n - 1
+    elif n < batch + 1:
+        raise ValueError(f"cu: {batch + 1} offsets expected, got {n}")
+    if total is None:
+        raise ValueError("total: the number of rows that cu may reach is needed with cu")
+    return batch, total, cu.data_ptr()
 
 
 def _vec(t, cache, batch, name):
     """Address of an optional int32 [batch] tensor."""
     if t is None:
         return None
-    _need(t, torch.int32, cache.device, name, (None,))
-    if t.shape[0] < batch:
-        raise ValueError(f"{name}: {batch} entries expected, got {t.shape[0]}")
+    if t.dtype is not torch.int32 or t.device != cache.device or t.dim() != 1 or not t.is_contiguous():
+        _need(t, torch.int32, cache.device, name, (None,))
+    if t.numel() < batch:
+        raise ValueError(f"{name}: {batch} entries expected, got {t.numel()}")
     return t.data_ptr()
 
 
-def _on(cache, stream):
-    """Device of the cache made current, and the stream there."""
+def _need_ws(ws, cache):
+    """(address, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    if ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {cache.device} expected")
+    return ws.data_ptr(), ws.nbytes
+
+
+def _call(cache, stream, name, *args):
+    """An entry point's result, on the cache's device (made current for the call) and `stream`."""
     dev = cache.device.index
     if dev is None:
         raise ValueError(f"cache: a CUDA device expected, got {cache.device}")
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    fn = getattr(lib(), name)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(cache.ref(), *args, stream)
     else:
-        stream = _stream(stream)
-    return (_NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)), stream
-
-
-_NO_GUARD = contextlib.nullcontext()
+        with torch.cuda.device(dev):
+            rc = fn(cache.ref(), *args, stream)
+    if rc != FLEX_OK:
+        raise FlexError(rc, name)
 
 
 def flex_paged_store_kv(cache: FlexPagedCache, k_new, v_new, row_stride, cu_new, most, pos0=None, total=None,
                         batch=None, stream=None):
     """Quantise new rows into the slots behind ctx_len. cu_new: int32 [batch + 1] row offsets (then
     `total` rows are there) or None (`most` rows each)."""
-    batch, total = _rows_call(cache, cu_new, most, total, batch)
-    width = cache.n_kv_heads * cache.head_dim
-    _need_rows(k_new, torch.float16, cache.device, "k_new", total, row_stride, width)
-    _need_rows(v_new, torch.float16, cache.device, "v_new", total, row_stride, width)
-    pos0 = _vec(pos0, cache, batch, "pos0")
-    guard, st = _on(cache, stream)
-    with guard:
-        rc = lib().flex_paged_store_kv(cache.ref(), k_new.data_ptr(), v_new.data_ptr(), row_stride,
-                                       None if cu_new is None else cu_new.data_ptr(), batch, total, most,
-                                       pos0, st)
-    _check(rc, "flex_paged_store_kv")
+    batch, total, cu = _rows_call(cache, cu_new, most, total, batch)
+    width, dev = cache.n_kv_heads * cache.head_dim, cache.device
+    _need_rows(k_new, torch.float16, 2, dev, "k_new", total, row_stride, width)
+    _need_rows(v_new, torch.float16, 2, dev, "v_new", total, row_stride, width)
+    _call(cache, stream, "flex_paged_store_kv", k_new.data_ptr(), v_new.data_ptr(), row_stride, cu, batch, total, most,
+          _vec(pos0, cache, batch, "pos0"))
 
 
 def flex_paged_load_kv(cache: FlexPagedCache, k_out, v_out, row_stride, cu_rows, most, start=None, total=None,
                        batch=None, stream=None):
     """Dequantise slots start[b] + i (start None: 0) into rows cu_rows[b] + i."""
-    batch, total = _rows_call(cache, cu_rows, most, total, batch)
-    width = cache.n_kv_heads * cache.head_dim
-    _need_rows(k_out, torch.float16, cache.device, "k_out", total, row_stride, width)
-    _need_rows(v_out, torch.float16, cache.device, "v_out", total, row_stride, width)
-    start = _vec(start, cache, batch, "start")
-    guard, st = _on(cache, stream)
-    with guard:
-        rc = lib().flex_paged_load_kv(cache.ref(), k_out.data_ptr(), v_out.data_ptr(), row_stride,
-                                      None if cu_rows is None else cu_rows.data_ptr(), batch, total, most,
-                                      start, st)
-    _check(rc, "flex_paged_load_kv")
+    batch, total, cu = _rows_call(cache, cu_rows, most, total, batch)
+    width, dev = cache.n_kv_heads * cache.head_dim, cache.device
+    _need_rows(k_out, torch.float16, 2, dev, "k_out", total, row_stride, width)
+    _need_rows(v_out, torch.float16, 2, dev, "v_out", total, row_stride, width)
+    _call(cache, stream, "flex_paged_load_kv", k_out.data_ptr(), v_out.data_ptr(), row_stride, cu, batch, total, most,
+          _vec(start, cache, batch, "start"))
 
 
 def _size(n, what):
@@ -647,8 +651,7 @@ def _size(n, what):
 
 
 def flex_paged_attention_ws_bytes(cache: FlexPagedCache, n_heads, total, most, accumulate=False, batch=None) -> int:
-    guard, _ = _on(cache, 0)
-    with guard:
+    with torch.cuda.device(cache.device):
         n = lib().flex_paged_attention_ws_bytes(cache.ref(), n_heads, cache.batch if batch is None else batch, total,
                                                 most, 1 if accumulate else 0)
     return _size(n, "flex_paged_attention_ws_bytes")
@@ -658,25 +661,24 @@ def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_n
                          accumulate=False, total=None, batch=None, stream=None):
     """Attention of new tokens over the cached slots and their own fresh keys/values (k_new and
     v_new None: cross attention, over the slots alone). lse: fp32 [total][n_heads] or None."""
-    batch, total = _rows_call(cache, cu_new, most, total, batch)
+    batch, total, cu = _rows_call(cache, cu_new, most, total, batch)
     dev, dim = cache.device, cache.head_dim
-    _need_rows(q, torch.float16, dev, "q", total, q_stride, n_heads * dim)
-    _need_rows(o, torch.float16, dev, "o", total, n_heads * dim, n_heads * dim)
+    width, kv_width = n_heads * dim, cache.n_kv_heads * dim
+    half = torch.float16
+    _need_rows(q, half, 2, dev, "q", total, q_stride, width)
+    _need_rows(o, half, 2, dev, "o", total, width, width)
     if k_new is not None:
-        _need_rows(k_new, torch.float16, dev, "k_new", total, kv_stride, cache.n_kv_heads * dim)
+        _need_rows(k_new, half, 2, dev, "k_new", total, kv_stride, kv_width)
+        k_new = k_new.data_ptr()
     if v_new is not None:
-        _need_rows(v_new, torch.float16, dev, "v_new", total, kv_stride, cache.n_kv_heads * dim)
+        _need_rows(v_new, half, 2, dev, "v_new", total, kv_stride, kv_width)
+        v_new = v_new.data_ptr()
     if lse is not None:
-        _need_rows(lse, torch.float32, dev, "lse", total, n_heads, n_heads)
-    guard, st = _on(cache, stream)
-    with guard:
-        rc = lib().flex_paged_attention(cache.ref(), q.data_ptr(), q_stride, n_heads,
-                                        None if k_new is None else k_new.data_ptr(),
-                                        None if v_new is None else v_new.data_ptr(), kv_stride, o.data_ptr(),
-                                        None if lse is None else lse.data_ptr(),
-                                        None if cu_new is None else cu_new.data_ptr(), batch, total, most,
-                                        1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), st)
-    _check(rc, "flex_paged_attention")
+        _need_rows(lse, torch.float32, 4, dev, "lse", total, n_heads, n_heads)
+        lse = lse.data_ptr()
+    ws, size = _need_ws(ws, cache)
+    _call(cache, stream, "flex_paged_attention", q.data_ptr(), q_stride, n_heads, k_new, v_new, kv_stride, o.data_ptr(), lse,
+          cu, batch, total, most, 1 if accumulate else 0, ws, size)
 
 
 def flex_paged_evict_ws_bytes(cache: FlexPagedCache, budget) -> int:
@@ -687,11 +689,8 @@ def flex_paged_evict(cache: FlexPagedCache, budget, recent, new_len, ws, stream=
     """Keep `budget` slots of every longer sequence and key head: the `recent` latest positions, then
     the largest weights. new_len (int32 [batch]) takes min(ctx_len, budget)."""
     _need(new_len, torch.int32, cache.device, "new_len", (cache.batch,))
-    guard, st = _on(cache, stream)
-    with guard:
-        rc = lib().flex_paged_evict(cache.ref(), budget, recent, new_len.data_ptr(), ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), st)
-    _check(rc, "flex_paged_evict")
+    ws, size = _need_ws(ws, cache)
+    _call(cache, stream, "flex_paged_evict", budget, recent, new_len.data_ptr(), ws, size)
 
 
 def flex_abi_layout(which: int, field: int) -> int:
