@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int item = blockIdx.x * S::WARPS + warp, share = A.plan.share;
     const int head = item % A.plan.heads;
-    const Unit u = find_unit<R, kRowsKeys, kRowsMin, 1>(c, A.rows, A.plan, item / A.plan.heads);
+    const Unit u = find_unit<R, kRowsKeys, kRowsMin, 1, false>(c, A.rows, A.plan, item / A.plan.heads);
     record_split<R, kRowsKeys>(A, u, item / A.plan.heads, head);
     if (!u.live) return;
     const int blocks = (u.ctx + kRowsKeys - 1) / kRowsKeys;
@@ -165,10 +165,10 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     for (int n = 0; n < NR; ++n) {
         const int r = row0 + n * 8 + g;
         const bool ok = r < row_end;
-        const int i = ok ? r / share : 0, h = ok ? head * share + r % share : 0;
+        const int i = ok ? token_of(A.plan, r) : 0, h = ok ? head * share + r - i * share : 0;
         load_query<D, BITS>(bq[n], A.q + static_cast<int64_t>(u.first + i) * A.q_stride + h * D, t, ok);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) token[n][e] = (row0 + n * 8 + 2 * t + e) / share;
+        for (int e = 0; e < 2; ++e) token[n][e] = token_of(A.plan, row0 + n * 8 + 2 * t + e);
     }
 
     float m[NR][2], l[NR][2], acc[D / 16][NR][4];
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
             const int r = n * 8 + 2 * t + e;
             if (row0 + r >= row_end) continue;
             if (u.parts == 1) {
-                const int64_t at = static_cast<int64_t>(u.first + token[n][e]) * (A.plan.heads * share) + head * share + (row0 + r) % share;
+                const int64_t at = static_cast<int64_t>(u.first + token[n][e]) * (A.plan.heads * share) + head * share + row0 + r - token[n][e] * share;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 uint32_t w[D / 16];
 #pragma unroll
@@ -484,25 +484,25 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 // of the codes and their conversion again (32 sequences of 500 to 1999 slots, 32 heads of
 // 64: 72 us with the kernel below).
 __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
-    pdl_wait();
     pdl_trigger();
     const PagedView& c = A.c;
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
-    if (rows_of(A.rows, b, first, c.status) == 0) return;
+    const int n = rows_of(A.rows, b, first, c.status);
     const int ctx = slots_of(c, b), held = ctx + (A.fresh != nullptr && A.k_new != nullptr);
     const int s0 = (blockIdx.x * 128 + threadIdx.x) * 4;      // four slots of one page
-    if (s0 >= held) return;
-    if (s0 >= paged_capacity(c)) {
-        paged_bad(c);                                         // no slot for the new token
+    const bool live = n > 0 && s0 < held, fits = s0 < paged_capacity(c);
+    if (live && !fits) paged_bad(c);                          // no slot for the new token
+    const int p = live && fits ? page_of(c, b, s0) : -1;
+    if (p < 0) {
+        pdl_wait();                                           // (a launch that ends is one whose predecessors have ended)
         return;
     }
-    const int p = page_of(c, b, s0);
-    if (p < 0) return;
     const int64_t row = slot_row(c, p, head, s0);
-    const float norm = __ldg(A.lse + static_cast<int64_t>(first) * A.plan.heads + head) * kLog2e;
-    const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
     float4 w = *reinterpret_cast<const float4*>(c.weight + row);
+    pdl_wait();                                               // the attention kernel writes what follows
+    const float norm = A.lse[static_cast<int64_t>(first) * A.plan.heads + head] * kLog2e;
+    const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
     const float fresh = s0 + 4 > ctx && held > ctx ? exp2_fast(fmaf(A.fresh[b * A.plan.heads + head], kLog2e, -norm)) : 0.f;
     auto one = [&](float& x, float score, int s) {
         if (s < ctx) x += exp2_fast(fmaf(score, kLog2e, -norm));
@@ -529,7 +529,6 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     constexpr int KB = D * BITS / 8, NG = D / GS, QR = 32, LD = D + 8;
     __shared__ __align__(16) __half sq[2][QR * LD];
     __shared__ float sl[2][QR];
-    pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, b = blockIdx.z;
@@ -539,25 +538,33 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     const bool fresh = static_cast<int>(blockIdx.x) >= old_blocks;
     const int j0 = (static_cast<int>(blockIdx.x) - (fresh ? old_blocks : 0)) * 128 + warp * 32;    // slot, or fresh token
     const int jend = fresh ? (k_new ? n : 0) : ctx;
-    if (j0 - warp * 32 >= jend || n == 0) return;       // a sequence without new tokens keeps its weights
+    if (j0 - warp * 32 >= jend || n == 0) {             // a sequence without new tokens keeps its weights
+        pdl_wait();                                     // (a launch that ends is one whose predecessors have ended)
+        return;
+    }
     // rows of the tokens that see any of the block's keys
     const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
     const int tiles = (row_end - row_lo + QR - 1) / QR;
-    auto load_rows = [&](int s) {
+    auto load_q = [&](int s) {
         for (int i = tid; i < QR * (D / 8); i += 128) {
             const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
             const bool ok = r < row_end;
-            const int tok = ok ? r / plan.share : 0, h = ok ? head * plan.share + r % plan.share : 0;
+            const int tok = ok ? token_of(plan, r) : 0, h = ok ? head * plan.share + r - tok * plan.share : 0;
             cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
-        }
-        if (tid < QR) {
-            const int r = row_lo + s * QR + tid;
-            const int tok = r / plan.share, h = head * plan.share + r % plan.share;
-            sl[s & 1][tid] = r < row_end ? __ldg(lse + static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h) * kLog2e : INFINITY;
         }
         cp_commit();
     };
-    load_rows(0);                                       // on their way while the keys are made operands
+    auto load_lse = [&](int s) {
+        if (tid < QR) {
+            const int r = row_lo + s * QR + tid;
+            const int tok = token_of(plan, r), h = head * plan.share + r - tok * plan.share;
+            sl[s & 1][tid] = r < row_end ? lse[static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h] * kLog2e : 0.f;
+        }
+    };
+    // All that the attention kernel does not write is requested before it is waited for: the
+    // first queries, and the keys, which become operands (in the order of the dims, as the
+    // queries' are) meanwhile.
+    load_q(0);
     int row[4];                                         // pool rows of keys j0 + g + 8 i, -1: none
     uint32_t a[2][D / 16][4];
     const int kgrp = t * (D / 4) / GS;
@@ -592,54 +599,65 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
             const uint4* x = reinterpret_cast<const uint4*>(k_new + static_cast<int64_t>(first + (j < jend ? j : 0)) * kv_stride +
                                                             head * D + t * (D / 4));
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) key_pairs_fresh<BITS>(pr[w], j < jend ? __ldg(x + w) : make_uint4(0, 0, 0, 0));
+            for (int w = 0; w < D / 32; ++w) key_pairs_fresh<8>(pr[w], j < jend ? __ldg(x + w) : make_uint4(0, 0, 0, 0));
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            a[i / 2][2 * w][i % 2] = pr[w][0];
-            a[i / 2][2 * w][2 + i % 2] = pr[w][1];
-            a[i / 2][2 * w + 1][i % 2] = pr[w][2];
-            a[i / 2][2 * w + 1][2 + i % 2] = pr[w][3];
+            // at 4 bits the pairs are (d, d + 4): neighbours again
+            const bool nibbles = BITS == 4 && !fresh;
+            a[i / 2][2 * w][i % 2] = nibbles ? byte_perm(pr[w][0], pr[w][1], 0x5410u) : pr[w][0];
+            a[i / 2][2 * w][2 + i % 2] = nibbles ? byte_perm(pr[w][2], pr[w][3], 0x5410u) : pr[w][1];
+            a[i / 2][2 * w + 1][i % 2] = nibbles ? byte_perm(pr[w][0], pr[w][1], 0x7632u) : pr[w][2];
+            a[i / 2][2 * w + 1][2 + i % 2] = nibbles ? byte_perm(pr[w][2], pr[w][3], 0x7632u) : pr[w][3];
         }
     }
+    pdl_wait();
+    load_lse(0);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    // 8 rows and the warp's 32 keys; ALL: every row sees every key
+    auto rows8 = [&](int s, int u, auto all_c) {
+        constexpr bool ALL = decltype(all_c)::value;
+        const int r0 = row_lo + s * QR + u * 8;
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const __half* qr = &sq[s & 1][(u * 8 + g) * LD + t * (D / 4)];
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            const uint4 z = *reinterpret_cast<const uint4*>(qr + w * 8);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mma168(sc[k], a[k][2 * w], z.x, z.y);
+                mma168(sc[k], a[k][2 * w + 1], z.z, z.w);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + 2 * t + e;
+            const float lr = sl[s & 1][u * 8 + 2 * t + e];
+            // the last key that the row sees; a row behind the last one sees none
+            const int seen = ALL ? 0 : r >= row_end ? -1 : fresh ? token_of(plan, r) : INT32_MAX;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float p = exp2_fast(fmaf(sc[k][2 * hh + e], kLog2e, -lr));
+                    if (ALL || j0 + k * 16 + hh * 8 + g <= seen) sum[2 * k + hh] += p;
+                }
+        }
+    };
     for (int s = 0; s < tiles; ++s) {
-        if (s + 1 < tiles)
-            load_rows(s + 1);
-        else
+        if (s + 1 < tiles) {
+            load_q(s + 1);
+            load_lse(s + 1);
+        } else {
             cp_commit();
+        }
         cp_wait<1>();
         __syncthreads();
+        if (!fresh && row_lo + (s + 1) * QR <= row_end) {
 #pragma unroll
-        for (int u = 0; u < QR / 8; ++u) {
-            const int r0 = row_lo + s * QR + u * 8;
-            if (r0 >= row_end) break;
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const __half* qr = &sq[s & 1][(u * 8 + g) * LD + t * (D / 4)];
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t z[4];
-                key_pairs_fresh<BITS>(z, *reinterpret_cast<const uint4*>(qr + w * 8));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    mma168(sc[k], a[k][2 * w], z[0], z[1]);
-                    mma168(sc[k], a[k][2 * w + 1], z[2], z[3]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 2 * t + e;
-                const float lr = sl[s & 1][u * 8 + 2 * t + e];      // +inf behind the last row: no weight
-                const int tok = fresh ? r / plan.share : INT32_MAX;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const float p = exp2_fast(fmaf(sc[k][2 * hh + e], kLog2e, -lr));
-                        const int j = j0 + k * 16 + hh * 8 + g;
-                        sum[2 * k + hh] += j <= tok ? p : 0.f;
-                    }
-            }
+            for (int u = 0; u < QR / 8; ++u) rows8(s, u, std::true_type{});
+        } else {
+            for (int u = 0; u < QR / 8 && row_lo + s * QR + u * 8 < row_end; ++u) rows8(s, u, std::false_type{});
         }
         __syncthreads();
     }
@@ -733,7 +751,9 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     AttnArgs a{};
     a.c = paged_view(cache);
     a.rows = RowsOf{cu_new, most, total};
-    a.plan = RowsPlan{batch, p.share, p.target, kvh};
+    a.plan = RowsPlan{batch, p.share, p.target, kvh, 0u};
+    if (p.share > 1 && (static_cast<int64_t>(most) * p.share + 512) * p.share < (1LL << 32))     // (+ 512: rows of a last tile)
+        a.plan.share_inverse = static_cast<uint32_t>((1ULL << 32) / p.share + 1);
     a.q = static_cast<const __half*>(q);
     a.q_stride = q_stride;
     a.k_new = static_cast<const __half*>(k_new);

@@ -127,7 +127,15 @@ __device__ __forceinline__ uint4 without_wild(uint4 x) {
 // 2 target / heads: only those have a slot for partial results.
 struct RowsPlan {
     int batch, share, target, heads;
+    uint32_t share_inverse;             // floor(2^32 / share) + 1 where rows * share < 2^32; else 0
 };
+
+// Row / share: with r (share_inverse * share - 2^32) <= r share < 2^32 the high product is the
+// quotient. A division takes some 20 instructions, and rows are divided all the time.
+__device__ __forceinline__ int token_of(const RowsPlan& p, int r) {
+    if (p.share == 1) return r;
+    return p.share_inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.share_inverse)) : r / p.share;
+}
 
 struct Unit {
     int b, tile, part, parts, per;      // per: key blocks in a part
@@ -140,8 +148,9 @@ struct Unit {
 // MIN: blocks of keys that a part has at least; less costs more to join than it saves.
 // FULL: where the tiles alone take more than half of the target, parts are as long as FULL
 // times an even share of the work: short enough to level the blocks' ends, and 1 or 2 by
-// what starting and joining a part costs beside its keys.
-template <int R, int KEYS, int MIN, int FULL>
+// what starting and joining a part costs beside its keys. SORT: the units of a batch of up
+// to 32 are in descending order of their keys, so that short blocks fill the end.
+template <int R, int KEYS, int MIN, int FULL, bool SORT>
 __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows, const RowsPlan& p, int unit) {
     const int lane = threadIdx.x & 31;
     struct Seq {
@@ -176,6 +185,20 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
     const int64_t even = (work * p.heads + room - 1) / room;
     Unit u{};
     u.plan_per = static_cast<int>(even < MIN ? MIN : even > (1 << 30) ? (1 << 30) : even);
+    // the unit is the at-th of lane l's sequence, whose partial slots begin at `slots`
+    auto found = [&](int l, int at, int b0, int parts, int slots) {
+        u.b = b0 + l;
+        u.n = __shfl_sync(0xffffffffu, q.n, l);
+        u.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
+        u.first = __shfl_sync(0xffffffffu, q.first, l);
+        u.parts = __shfl_sync(0xffffffffu, parts, l);
+        u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
+        u.slot = slots + at;
+        u.tile = at / u.parts;
+        u.part = at % u.parts;
+        u.live = true;
+        return u;
+    };
     int64_t before = 0, split = 0;                      // units, and units of split tiles, of the sequences passed
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         if (b0 > 0) q = load(b0 + lane);
@@ -189,6 +212,19 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
             split += sum2;
             continue;
         }
+        if (SORT && p.batch <= 32) {
+            const int cost = (q.ctx + KEYS - 1) / KEYS / parts + q.n / KEYS;
+            int x = 0, y = 0;                           // units of the sequences in front of b
+            for (int i = 0; i < p.batch; ++i) {
+                const int c2 = __shfl_sync(0xffffffffu, cost, i), m = __shfl_sync(0xffffffffu, mine, i),
+                          m2 = __shfl_sync(0xffffffffu, mine2, i);
+                const bool front = c2 > cost || (c2 == cost && i < lane);
+                x += front ? m : 0;
+                y += front ? m2 : 0;
+            }
+            const int l = __ffs(__ballot_sync(0xffffffffu, unit >= x && unit < x + mine)) - 1;
+            return found(l, unit - __shfl_sync(0xffffffffu, x, l), b0, parts, __shfl_sync(0xffffffffu, y, l));
+        }
         int x = mine, y = mine2;                        // up to and with b
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -201,17 +237,7 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
         const int want = static_cast<int>(unit - before);
         const int l = __ffs(__ballot_sync(0xffffffffu, want < x)) - 1;
         const int at = want - __shfl_sync(0xffffffffu, x - mine, l);
-        u.b = b0 + l;
-        u.n = __shfl_sync(0xffffffffu, q.n, l);
-        u.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
-        u.first = __shfl_sync(0xffffffffu, q.first, l);
-        u.parts = __shfl_sync(0xffffffffu, parts, l);
-        u.per = max(1, ((u.ctx + KEYS - 1) / KEYS + u.parts - 1) / u.parts);     // even parts
-        u.slot = static_cast<int>(split) + __shfl_sync(0xffffffffu, y - mine2, l) + at;
-        u.tile = at / u.parts;
-        u.part = at % u.parts;
-        u.live = true;
-        return u;
+        return found(l, at, b0, parts, static_cast<int>(split) + __shfl_sync(0xffffffffu, y - mine2, l));
     }
     return u;
 }
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
 #pragma unroll
                 for (int i = 1; i < G; ++i) add(part_stat[i], part_out[i][threadIdx.x]);
             }
-            const int tok = (row0 + r) / plan.share, h = head * plan.share + (row0 + r) % plan.share;
+            const int tok = token_of(plan, row0 + r), h = head * plan.share + row0 + r - tok * plan.share;
             const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     pdl_wait();
     pdl_trigger();
     const int head = blockIdx.x % A.plan.heads;
-    const Unit u = find_unit<R, 128, kTileMin, 2>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
+    const Unit u = find_unit<R, 128, kTileMin, 2, true>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
     if (warp == 0) record_split<R, 128>(A, u, blockIdx.x / A.plan.heads, head);
     if (!u.live) return;
     const int share = A.plan.share;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         // ---- softmax: one row a thread
         const int tile = warp >> 2, r = tid & 127, row = row0 + tile * 128 + r;
         const bool live = row < row_end;
-        const int token = live ? row / share : 0, h = head * share + (live ? row % share : 0);
+        const int token = live ? token_of(A.plan, row) : 0, h = head * share + (live ? row - token * share : 0);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + TILES * 128 + tile * D + lanes;
         bool ok = tile < tiles;
