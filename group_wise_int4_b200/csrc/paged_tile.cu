@@ -120,9 +120,11 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             tc::bar_init(k_full + 8 * i, 2);          // one arrival a warp
-            tc::bar_init(k_empty + 8 * i, tiles);
+            // S_j has read its keys: the softmax warps know first, the score warps with (P V)_j, which is
+            // soon enough with 4 stages and takes nothing from the softmax
+            tc::bar_init(k_empty + 8 * i, ST > 2 ? tiles : 4 * tiles);
             tc::bar_init(v_full + 8 * i, 2);
-            tc::bar_init(v_empty + 8 * i, tiles);
+            tc::bar_init(v_empty + 8 * i, tiles);       // from the score warps, which see (P V)_j
         }
         tc::bar_init(q_full, 4 * tiles);
         for (int t = 0; t < TILES; ++t) {
@@ -178,6 +180,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             arrive(q_full);
             for (int j = 0; j < nb; ++j) {
                 if (!(ok = wait(s_full + 16 * tile + 8 * (j & 1), (j >> 1) & 1))) break;
+                if (ST <= 2 && j + ST < nb) arrive(k_empty + 8 * (j % ST));
                 tc::fence_after_sync();
                 // keys of the block that this row sees: the first `lim`
                 const int lim = j < nc ? key1 - key0 - j * NK : token + 1 - (j - nc) * NK;
@@ -403,6 +406,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         const bool value = (warp - SOFT - 4) & 1;
         const uint32_t leader = lane == 0, td = tmem + t * 128;
         bool ok = true;
+        uint32_t last_bar = 0, last_phase = 0;                  // of the last commit
         auto wait1 = [&](uint32_t bar, uint32_t parity) {
             ok = ok && wait(bar, parity);
             return ok;
@@ -414,8 +418,14 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             ok = nb == 0 || wait(q_full, 0);
             for (int j = 0; j < nb && ok; ++j) {
                 const int s = j % ST, h = j & 1;
+                if (j > 1) {
+                    if (!wait1(o_done + 16 * t + 8 * h, ((j - 2) >> 1) & 1)) break;
+                    if (j - 2 + ST < nb) {                      // (P V)_(j-2) has read its values
+                        arrive(v_empty + 8 * ((j - 2) % ST));
+                        if (ST > 2) arrive(k_empty + 8 * ((j - 2) % ST));
+                    }
+                }
                 if (!wait1(k_full + 8 * s, (j / ST) & 1)) break;
-                if (j > 1 && !wait1(o_done + 16 * t + 8 * h, ((j - 2) >> 1) & 1)) break;
                 tc::fence_after_sync();
                 const uint64_t b = dk + s * (T::BLOCK >> 4);
 #pragma unroll
@@ -423,7 +433,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     tc::mma_f16_if(leader, td + h * NK, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                    b + (((k >> 2) * (NK * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
                 tc::mma_commit_if(leader, s_full + 16 * t + 8 * h);
-                if (j + ST < nb) tc::mma_commit_if(leader, k_empty + 8 * s);
+                last_bar = s_full + 16 * t + 8 * h;
+                last_phase = (j >> 1) & 1;
             }
         } else {
             constexpr uint32_t idesc = tc::idesc_f16_f32(128, D) | tc::kIdescBMnMajor;
@@ -438,13 +449,17 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     tc::mma_f16_ts_if(leader, tmem + TILES * 128 + t * D, td + h * NK + k * 8, b + k * (2048 >> 4), idesc,
                                       j > 0 || k > 0);
                 tc::mma_commit_if(leader, o_done + 16 * t + 8 * h);
-                if (j + ST < nb) tc::mma_commit_if(leader, v_empty + 8 * s);
+                last_bar = o_done + 16 * t + 8 * h;
+                last_phase = (j >> 1) & 1;
             }
         }
         if (!ok) {                                              // what was issued reads shared memory: let it end
+            volatile int never = 0;
             const uint32_t bar = drain + 8 * (warp - SOFT - 4);
             tc::mma_commit_if(leader, bar);
-            wait(bar, 0);
+            tc::bar_wait(bar, 0, &never, status, wait_ns);
+            if (last_bar != 0) tc::bar_wait(last_bar, last_phase, &never, status, wait_ns);
+            __syncwarp();
         }
     }
     tc::fence_before_sync();
