@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 tc::fence_before_sync();
                 arrive(p_full + 16 * tile + 8 * (j & 1));
             }
+            // (both: no arrival of a commit is still to come when the block's shared memory is given up)
+            if (ok && nb > 1) ok = wait(o_done + 16 * tile + 8 * (nb & 1), ((nb - 2) >> 1) & 1);
             if (ok && nb > 0) ok = wait(o_done + 16 * tile + 8 * ((nb - 1) & 1), ((nb - 1) >> 1) & 1);
             tc::fence_after_sync();
         }
@@ -418,14 +420,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             ok = nb == 0 || wait(q_full, 0);
             for (int j = 0; j < nb && ok; ++j) {
                 const int s = j % ST, h = j & 1;
-                if (j > 1) {
-                    if (!wait1(o_done + 16 * t + 8 * h, ((j - 2) >> 1) & 1)) break;
-                    if (j - 2 + ST < nb) {                      // (P V)_(j-2) has read its values
-                        arrive(v_empty + 8 * ((j - 2) % ST));
-                        if (ST > 2) arrive(k_empty + 8 * ((j - 2) % ST));
-                    }
-                }
                 if (!wait1(k_full + 8 * s, (j / ST) & 1)) break;
+                if (j > 1 && !wait1(o_done + 16 * t + 8 * h, ((j - 2) >> 1) & 1)) break;
                 tc::fence_after_sync();
                 const uint64_t b = dk + s * (T::BLOCK >> 4);
 #pragma unroll
@@ -435,6 +431,10 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 tc::mma_commit_if(leader, s_full + 16 * t + 8 * h);
                 last_bar = s_full + 16 * t + 8 * h;
                 last_phase = (j >> 1) & 1;
+                if (j > 1 && j - 2 + ST < nb) {                 // (P V)_(j-2) has read its values
+                    arrive(v_empty + 8 * ((j - 2) % ST));
+                    if (ST > 2) arrive(k_empty + 8 * ((j - 2) % ST));
+                }
             }
         } else {
             constexpr uint32_t idesc = tc::idesc_f16_f32(128, D) | tc::kIdescBMnMajor;

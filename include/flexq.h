@@ -338,8 +338,9 @@ int flex_layernorm(const void* x, const void* g, const void* b, void* y, int64_t
  *             in each slot (written by flex_paged_store_kv, used by flex_paged_evict).
  *   page_table: device int32 [batch][max_pages]; slot s of sequence b is slot
  *             s % page_size of page page_table[b][s / page_size]. Entries behind a
- *             sequence's last page are not read. Two sequences may share pages that no
- *             call writes.
+ *             sequence's last page are not read. Sequences may share pages that no call
+ *             writes (the store writes new slots' pages, accumulate every page of the
+ *             sequences with new tokens, eviction all of them).
  *   ctx_len : device int32 [batch], slots that each sequence holds before the call. No call
  *             changes it (the layers of a model share it): the caller adds the new tokens,
  *             or takes flex_paged_evict's new_len, once every layer is done.
@@ -395,8 +396,12 @@ int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, void* v_out, 
  *   weight[slot] = (slot < ctx_len ? weight[slot] : 0) + sum of p over the sequence's new
  *   tokens and the heads that share the key head, for the slots [0, ctx_len + new tokens)
  *   (cross attention: [0, ctx_len)). Each slot's sum has a fixed order.
+ * Infinities and NaN of a key or value reach the rows that attend to it, and no other row.
  * ws: flex_paged_attention_ws_bytes(...) bytes, nothing in it has to be set; calls that may
- * run at the same time need workspaces of their own. Strides are multiples of 8. */
+ * run at the same time need workspaces of their own. (With accumulate and one row a
+ * sequence and key head, 4 bytes for every slot of the pool: the scores.) Strides are
+ * multiples of 8. Waits inside the kernels are bounded (flex_set_wait_limit_ns):
+ * FLEX_ERR_TIMEOUT by flex_get_status. */
 int64_t flex_paged_attention_ws_bytes(const flex_paged_cache* cache, int32_t n_heads, int32_t batch, int32_t total,
                                       int32_t most, int32_t accumulate);
 int flex_paged_attention(const flex_paged_cache* cache, const void* q, int64_t q_stride, int32_t n_heads,
@@ -411,7 +416,7 @@ int flex_paged_attention(const flex_paged_cache* cache, const void* q, int64_t q
  * metadata, weight and position of the i-th kept slot behind it; nothing else moves, and
  * slots from the budget on keep their old contents. new_len[b] = min(ctx_len[b], budget)
  * (device int32 [batch], not overlapping ctx_len). 0 <= recent <= budget, budget > 0.
- * Needs weight and slot_pos. A page must belong to one sequence only. Heads hold
+ * Needs weight and slot_pos. A page must belong to one sequence only, and once. Heads hold
  * different tokens afterwards, in no order: attention over the cache needs none.
  * ws: flex_paged_evict_ws_bytes(cache, budget) bytes, as for the attention. */
 int64_t flex_paged_evict_ws_bytes(const flex_paged_cache* cache, int32_t budget);
