@@ -686,7 +686,11 @@ AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total,
     AttnPlan p{};
     p.share = n_heads / c->n_kv_heads;
     const int64_t rows = static_cast<int64_t>(most) * p.share;
-    p.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
+    // Row tiles of 16 up to 32 rows, though each of two turns the codes into operands by itself, tcgen05
+    // tiles above. us with 16-row / 128-row tiles for 8 sequences of 2000 slots at 16 heads of 64, 32 of
+    // 1000 at 32 of 128, 4 of 16000 at 8 of 128 and 8 bits: 17 rows 30 / 35, 123 / 160, 62 / 88; 32 rows
+    // 33 / 32, 126 / 161, 64 / 89; 33 rows 43 / 36, 185 / 161, 89 / 91.
+    p.row_tile = rows <= 8 ? 8 : rows <= 32 ? 16 : paged_tile_rows(rows > 1024 ? 1024 : static_cast<int>(rows));
     // units times heads wanted: what the device holds at once
     p.target = p.row_tile <= 16 ? rows_warps(c->head_dim, p.row_tile) * sm_count() : paged_tile_target(p.row_tile);
     // every sequence's row tiles, and what their parts add (the bounds stand at find_unit)
