@@ -3,8 +3,8 @@
 // For row r (token i of sequence b, query head h, key head g = h / share):
 //   s_j = q_r . k_j over the slots j < ctx_len[b] and the fresh tokens 0..i,
 //   lse_r = log sum_j exp(s_j),  o_r = sum_j exp(s_j - lse_r) v_j,
-// in one pass over the keys with a running maximum and sum; statistics are fp32 and in
-// base 2 (scores times log2 e), probabilities are rounded to fp16 once, as operands of the
+// in one pass over the keys with a running maximum and sum; statistics are fp32,
+// probabilities are rounded to fp16 once, as operands of the
 // value product: at most 2^-11 of each, far below o's own fp16 rounding after the sum.
 // k_j and v_j are the fp16 values of paged.cuh, so the products are exact and summed in fp32.
 #include <type_traits>
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 
     // Scores of T tiles of 16 keys (-inf where hidden) -> running maximum, sum, and the
     // probabilities as the value product's operand. The maximum moves only when a score
-    // passes it by more than 2^8: until then probabilities are up to 256, with the same
+    // passes it so far that its weight would pass 2^8: until then probabilities are up to 256, with the same
     // relative error, and nothing is rescaled.
     auto softmax = [&](auto& sc, auto& pb, auto tiles_c) {
         constexpr int T = decltype(tiles_c)::value;
@@ -196,15 +196,14 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
                 top[e] = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
 #pragma unroll
                 for (int k = 1; k < T; ++k) top[e] = fmaxf(top[e], fmaxf(sc[k][n][e], sc[k][n][2 + e]));
-                top[e] *= kLog2e;
             }
-            if (__any_sync(0xffffffffu, top[0] > m[n][0] + 8.f || top[1] > m[n][1] + 8.f)) {
+            if (__any_sync(0xffffffffu, top[0] > m[n][0] + kSlack || top[1] > m[n][1] + kSlack)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], w));
-                    const bool moves = top[e] > m[n][e] + 8.f;      // a row's result depends on no other row
-                    const float f = moves ? exp2_fast(m[n][e] - top[e]) : 1.f;
+                    const bool moves = top[e] > m[n][e] + kSlack;      // a row's result depends on no other row
+                    const float f = moves ? exp2_fast(exponent_of(m[n][e], top[e])) : 1.f;
                     m[n][e] = moves ? top[e] : m[n][e];
                     l[n][e] *= f;
 #pragma unroll
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
             for (int k = 0; k < T; ++k) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(sc[k][n][e], kLog2e, -m[n][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(exponent_of(sc[k][n][e], m[n][e & 1]));
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];
                 pb[k][n][0] = mat_trans(half2_of(p[0], p[1]));
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 4)
                     *reinterpret_cast<uint4*>(A.o + at * D + g * (D / 8) + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                if (g == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (m[n][e] + log2f(sum)) * kLn2;
+                if (g == 0) put_stats(A, at, m[n][e], sum);
             } else if (u.slot < A.slots) {
                 float* p = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + r) * (D + 4);
 #pragma unroll
@@ -503,11 +502,11 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
     const int64_t row = slot_row(c, p, head, s0);
     float4 w = *reinterpret_cast<const float4*>(c.weight + row);
     pdl_wait();                                               // the attention kernel writes what follows
-    const float norm = A.lse[static_cast<int64_t>(first) * A.plan.heads + head] * kLog2e;
+    const float2 stats = A.stats[static_cast<int64_t>(first) * A.plan.heads + head];
     const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
-    const float fresh = s0 + 4 > ctx && held > ctx ? exp2_fast(fmaf(A.fresh[b * A.plan.heads + head], kLog2e, -norm)) : 0.f;
+    const float fresh = s0 + 4 > ctx && held > ctx ? prob_of(A.fresh[b * A.plan.heads + head], stats) : 0.f;
     auto one = [&](float& x, float score, int s) {
-        if (s < ctx) x += exp2_fast(fmaf(score, kLog2e, -norm));
+        if (s < ctx) x += prob_of(score, stats);
         else if (s < held) x = fresh;
     };
     one(w.x, sc.x, s0);
@@ -528,10 +527,9 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     const RowsPlan& plan = A.plan;
     const __half *q = A.q, *k_new = A.k_new;
     const int64_t q_stride = A.q_stride, kv_stride = A.kv_stride;
-    const float* lse = A.lse;
     constexpr int KB = D * BITS / 8, NG = D / GS, QR = 32, LD = D + 8;
     __shared__ __align__(16) __half sq[2][QR * LD];
-    __shared__ float sl[2][QR];
+    __shared__ float2 sl[2][QR];
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, b = blockIdx.z;
@@ -557,11 +555,11 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
         }
         cp_commit();
     };
-    auto load_lse = [&](int s) {
+    auto load_stats = [&](int s) {
         if (tid < QR) {
             const int r = row_lo + s * QR + tid;
             const int tok = token_of(plan, r), h = head * plan.share + r - tok * plan.share;
-            sl[s & 1][tid] = r < row_end ? lse[static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h] * kLog2e : 0.f;
+            sl[s & 1][tid] = r < row_end ? A.stats[static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h] : make_float2(0.f, 0.f);
         }
     };
     // All that the attention kernel does not write is requested before it is waited for: the
@@ -615,7 +613,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
         }
     }
     pdl_wait();
-    load_lse(0);
+    load_stats(0);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     // 8 rows and the warp's 32 keys; ALL: every row sees every key
     auto rows8 = [&](int s, int u, auto all_c) {
@@ -635,14 +633,14 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = r0 + 2 * t + e;
-            const float lr = sl[s & 1][u * 8 + 2 * t + e];
+            const float2 stats = sl[s & 1][u * 8 + 2 * t + e];
             // the last key that the row sees; a row behind the last one sees none
             const int seen = ALL ? 0 : r >= row_end ? -1 : fresh ? token_of(plan, r) : INT32_MAX;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const float p = exp2_fast(fmaf(sc[k][2 * hh + e], kLog2e, -lr));
+                    const float p = prob_of(sc[k][2 * hh + e], stats);
                     if (ALL || j0 + k * 16 + hh * 8 + g <= seen) sum[2 * k + hh] += p;
                 }
         }
@@ -650,7 +648,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     for (int s = 0; s < tiles; ++s) {
         if (s + 1 < tiles) {
             load_q(s + 1);
-            load_lse(s + 1);
+            load_stats(s + 1);
         } else {
             cp_commit();
         }
@@ -676,8 +674,8 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
 
 struct AttnPlan {
     int share, row_tile, target, slots;
-    int64_t units, records_bytes, parts_bytes, lse_bytes, fresh_bytes, score_bytes;
-    int64_t bytes() const { return records_bytes + parts_bytes + lse_bytes + fresh_bytes + score_bytes; }
+    int64_t units, records_bytes, parts_bytes, stats_bytes, fresh_bytes, score_bytes;
+    int64_t bytes() const { return records_bytes + parts_bytes + stats_bytes + fresh_bytes + score_bytes; }
 };
 
 inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -702,7 +700,7 @@ AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total,
     const bool one = accumulate && rows == 1;
     p.fresh_bytes = one ? up256(static_cast<int64_t>(batch) * n_heads * 4) : 0;
     p.score_bytes = one ? up256(static_cast<int64_t>(c->num_pages) * c->page_size * c->n_kv_heads * 4) : 0;
-    p.lse_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 4) : 0;
+    p.stats_bytes = accumulate ? up256(static_cast<int64_t>(total) * n_heads * 8) : 0;
     return p;
 }
 
@@ -771,10 +769,11 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     a.split_units = reinterpret_cast<int*>(w);
     a.records = reinterpret_cast<SplitRecord*>(w + 256);
     a.parts = reinterpret_cast<float*>(w + p.records_bytes);
-    a.lse = lse == nullptr && accumulate ? reinterpret_cast<float*>(w + p.records_bytes + p.parts_bytes) : lse;
+    a.lse = lse;
+    a.stats = accumulate ? reinterpret_cast<float2*>(w + p.records_bytes + p.parts_bytes) : nullptr;
     a.slots = p.slots;
     if (p.score_bytes > 0) {
-        w += p.records_bytes + p.parts_bytes + p.lse_bytes;
+        w += p.records_bytes + p.parts_bytes + p.stats_bytes;
         a.fresh = reinterpret_cast<float*>(w);
         a.scores = reinterpret_cast<float*>(w + p.fresh_bytes);
     }

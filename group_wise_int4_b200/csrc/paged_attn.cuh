@@ -248,7 +248,7 @@ struct SplitRecord {
 };
 
 // What a launch of either attention kernel gets. Partial results: [slot][head][row of the
-// tile][D + 4]: the output, then the maximum (base 2) and the sum.
+// tile][D + 4]: the output, then the maximum and the sum.
 struct AttnArgs {
     PagedView c;
     RowsOf rows;
@@ -259,6 +259,7 @@ struct AttnArgs {
     int64_t kv_stride;
     __half* o;
     float* lse;
+    float2* stats;              // weights wanted: maximum and log2 of the sum of each row and head; else nullptr
     float* parts;
     float *scores, *fresh;      // one row a sequence and key head, weights wanted: its scores, by slot's row and
                                 // of its own token [batch][heads]; else nullptr
@@ -266,6 +267,22 @@ struct AttnArgs {
     SplitRecord* records;       // [slots]
     int slots;                  // of partial results
 };
+
+// Exponent (base 2) of a score's weight relative to m. The difference comes first: it is exact
+// near the maximum and 0 at it, however large the scores are.
+__device__ __forceinline__ float exponent_of(float score, float m) { return (score - m) * kLog2e; }
+constexpr float kSlack = 8.f * kLn2;                // a maximum may be passed so far: weights up to 2^8
+
+// A row's statistics, at [row][head]: sum = 2^left times the sum of exp(score - top).
+__device__ __forceinline__ void put_stats(const AttnArgs& A, int64_t at, float top, float sum, float left = 0.f) {
+    const float l = log2f(sum) - left;
+    if (A.lse) A.lse[at] = sum == 0.f ? -INFINITY : fmaf(l, kLn2, top);
+    if (A.stats) A.stats[at] = make_float2(top, sum == 0.f ? INFINITY : l);
+}
+// The probability of a score, by these statistics.
+__device__ __forceinline__ float prob_of(float score, float2 stats) {
+    return exp2_fast(fmaf(score - stats.x, kLog2e, -stats.y));
+}
 
 // Called by one warp of every unit and head: unit 0 says how many partial slots there are, a
 // split unit where it belongs.
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
             float top = -FLT_MAX, sum = 0.f;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             auto add = [&](float2 ml, float4 x) {
-                const float t = fmaxf(top, ml.x), f0 = exp2_fast(top - t), f = exp2_fast(ml.x - t);
+                const float t = fmaxf(top, ml.x), f0 = exp2_fast(exponent_of(top, t)), f = exp2_fast(exponent_of(ml.x, t));
                 top = t;
                 sum = fmaf(sum, f0, f * ml.y);
                 a.x = fmaf(a.x, f0, f * x.x);
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
             const int64_t at = static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2*>(A.o + at * D + d) = make_uint2(half2_of(a.x * inv, a.y * inv), half2_of(a.z * inv, a.w * inv));
-            if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            if (d == 0) put_stats(A, at, top, sum);
         }
     }
 }

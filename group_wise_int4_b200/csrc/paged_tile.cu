@@ -24,8 +24,8 @@
 // unit is busy 1024. Tried and slower: the two tiles' exponentials in turns (1040), a
 // quarter of them as polynomials (1125), two threads a row.
 //
-// The running maximum m only moves when a score passes it by more than 2^8 (in base 2, 8
-// steps): until then the probabilities are up to 256 instead of 1, which fp16 holds with
+// The running maximum m only moves when a score passes it so far that its weight would pass
+// 2^8: until then the probabilities are up to 256 instead of 1, which fp16 holds with
 // the same relative error, and O is not rescaled. The final quotient does not depend on m.
 #include <type_traits>
 
@@ -84,6 +84,15 @@ __device__ __forceinline__ uint64_t f32x2_scale(uint64_t a, float f) {
 template <int ROWS>
 __device__ __forceinline__ uint32_t piece_at(uint32_t base, int r, int c) {
     return base + (c >> 3) * (ROWS * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16;
+}
+
+// Exponents are score * log2 e - fl(m log2 e), one fused multiply-add for each score: against
+// (score - m) log2 e every weight of the row is 2^leftover(m) times as large. A maximum of
+// 2^23 or more would leave factors that overflow: such rows' scores have m subtracted in
+// tensor memory first, and no shift.
+__device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= 8388608.f && m != -FLT_MAX; }
+__device__ __forceinline__ float leftover(float m) {
+    return m == -FLT_MAX || is_big(m) ? 0.f : fmaf(m, kLog2e, -__fmul_rn(m, kLog2e));
 }
 
 template <int D, int BITS, int GS, int TILES>
@@ -170,7 +179,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + TILES * 128 + tile * D + lanes;
         bool ok = tile < tiles;
-        float m = -FLT_MAX;
+        // the running maximum; the score from which it moves; what the fused exponent adds
+        float m = -FLT_MAX, limit = -FLT_MAX, shift = 0.f;
         uint64_t l = 0;                                          // two partial sums
         if (ok) {
             const uint4* qr = reinterpret_cast<const uint4*>(A.q + static_cast<int64_t>(u.first + token) * A.q_stride + h * D);
@@ -204,13 +214,16 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
 #pragma unroll
                     for (int i = 0; i < NK; i += 2)
                         tops[(i >> 1) & 3] = fmaxf(fmaxf(tops[(i >> 1) & 3], score(i)), score(i + 1));
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * kLog2e;
-                    if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                        const bool moves = top > m + 8.f;       // a row's result depends on no other row
-                        const float f = moves ? exp2_fast(m - top) : 1.f;
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    if (__any_sync(0xffffffffu, top > limit)) {
+                        const bool moves = top > m + kSlack;    // a row's result depends on no other row
+                        const float was = m, left = leftover(m);
                         m = moves ? top : m;
+                        const float f = moves ? exp2_fast(fmaf(was - m, kLog2e, leftover(m) - left)) : 1.f;
                         l = f32x2_scale(l, f);
-                        if (j > 0) {
+                        limit = is_big(m) ? -INFINITY : m + kSlack;
+                        shift = is_big(m) ? 0.f : -__fmul_rn(m, kLog2e);
+                        if (j > 0 && __any_sync(0xffffffffu, moves)) {
                             if (!(ok = wait(o_done + 16 * tile + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1))) return;
                             tc::fence_after_sync();
 #pragma unroll 1
@@ -222,8 +235,25 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                                 tc::tmem_st16(to + i, y);
                             }
                         }
+                        if (__any_sync(0xffffffffu, is_big(m))) {
+                            // S becomes S - m, and its shift is 0
+#pragma unroll 1
+                            for (int i = 0; i < NK; i += 16) {
+                                uint32_t y[16];
+                                tc::tmem_ld16(tj + i, y);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (is_big(m)) y[k] = __float_as_uint(__uint_as_float(y[k]) - m);
+                                tc::tmem_st16(tj + i, y);
+                            }
+                            tc::tmem_wait_st();
+                            tc::tmem_ld32(tj, x[0]);
+                            tc::tmem_ld32(tj + 32, x[1]);
+                            tc::tmem_wait_ld(x[0]);
+                            tc::tmem_wait_ld(x[1]);
+                        }
                     }
-                    const uint64_t scale = f32x2(kLog2e, kLog2e), shift = f32x2(-m, -m);
+                    const uint64_t scale2 = f32x2(kLog2e, kLog2e), shift2 = f32x2(shift, shift);
                     uint64_t sums[2] = {l, 0};
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -231,7 +261,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float y0, y1;
-                            f32x2_get(f32x2_fma(f32x2(score(half * 32 + i), score(half * 32 + i + 1)), scale, shift), y0, y1);
+                            f32x2_get(f32x2_fma(f32x2(score(half * 32 + i), score(half * 32 + i + 1)), scale2, shift2), y0, y1);
                             const float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
                             sums[(i >> 1) & 1] = f32x2_add(sums[(i >> 1) & 1], f32x2(p0, p1));
                             const __half2 hp = __floats2half2_rn(p0, p1);
@@ -259,7 +289,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         f32x2_get(l, l0, sum);
         sum += l0;
         if (ok) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            // sum and O hold 2^leftover(m) times the weights relative to m; the quotient does not
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, even = exp2_fast(-leftover(m));
             const int64_t at = static_cast<int64_t>(u.first + token) * (A.plan.heads * share) + h;
             float* part = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + tile * 128 + r) * (D + 4);
             const bool wild = wild_flag != 0;
@@ -305,14 +336,14 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 } else if (u.slot < A.slots) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4*>(part + i + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        *reinterpret_cast<float4*>(part + i + 4 * k) = make_float4(v[4 * k] * even, v[4 * k + 1] * even, v[4 * k + 2] * even, v[4 * k + 3] * even);
                 }
             }
             if (live) {
                 if (u.parts > 1) {
-                    if (u.slot < A.slots) *reinterpret_cast<float2*>(part + D) = make_float2(m, sum);
-                } else if (A.lse) {
-                    A.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                    if (u.slot < A.slots) *reinterpret_cast<float2*>(part + D) = make_float2(m, sum * even);
+                } else {
+                    put_stats(A, at, m, sum, leftover(m));
                 }
             }
         }

@@ -626,3 +626,79 @@ def test_the_whole_batch_is_empty():
     c.attend([c.rows(0, 2), c.rows(0, 2)], [c.rows(0), c.rows(0)], [c.rows(0), c.rows(0)])
     o, ls = c.attend(_scaled(c, [2, 1], 2))
     assert not bool(o[:3].any()) and bool((ls[:3] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("dim,bits,group,page", SHAPES)
+@pytest.mark.parametrize("most", [12, 20, 64, 200])
+def test_every_row_tile(dim, bits, group, page, most):
+    """8 and 16 rows of the rows kernel, one and two of the latter's tiles, and 128 and 256 rows."""
+    ctx = [0, 63, 64, 65, 300]
+    n = [most, 1, most // 2, 0, most - 3]
+    c = Case(30 + most, ctx, heads=2, dim=dim, bits=bits, group=group, page=page, room=most)
+    c.attend(_scaled(c, n, 2), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+    c.attend(_scaled(c, n, 2))
+
+
+@pytest.mark.parametrize("most", [30, 100, 290])
+def test_long_histories_are_split(most):
+    """Few sequences: the tiles' keys are cut into parts and joined."""
+    c = Case(31, [4000, 10, 2300], heads=1, dim=64, bits=4, group=64, page=64, room=most)
+    n = [most, 2, most // 3]
+    c.attend(_scaled(c, n, 1), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+    c.attend(_scaled(c, n, 1))
+
+
+def test_many_ragged_sequences():
+    """More sequences than a warp has lanes, with tiles of 128 rows and with splits."""
+    ctx = [(37 * i) % 260 for i in range(45)] + [3100]
+    c = Case(32, ctx, heads=1, dim=128, bits=8, group=64, page=32, room=41)
+    n = [(5 * i) % 41 for i in range(45)] + [40]
+    c.attend(_scaled(c, n, 1), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_evict_tables_of_several_kinds(dim):
+    """Up to 2048 slots a table, few and many moves, and more slots."""
+    for seed, ctx, page, room, budget, recent in ((33, [2048, 2000, 9], 1024, 0, 2040, 100), (34, [2048, 1100], 128, 0, 700, 650),
+                                                  (35, [2100, 3000, 50], 64, 200, 1000, 30), (36, [1500], 16, 0, 1499, 0)):
+        _evict(Case(seed, ctx, heads=2, dim=dim, bits=4, group=32, page=page, room=room), budget, recent)
+
+
+def test_one_sequence_of_the_table():
+    """batch smaller than the table's: the first sequences alone."""
+    c = Case(37, [70, 30, 5], heads=2, room=3)
+    q, k, v = _scaled(c, [2], 2), [c.rows(2)], [c.rows(2)]
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    o = torch.empty((total, 2 * c.dim), dtype=torch.float16, device="cuda")
+    ls = torch.empty((total, 2), device="cuda")
+    for b, rows in ((None, cu), (1, None)):
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 2, total, most, batch=1), dtype=torch.uint8, device="cuda")
+        fq.flex_paged_attention(c.cache, qd, qd.stride(0), 2, kd, vd, kd.stride(0), o, ls, rows, most, ws, total=total, batch=b)
+        sync_status()
+        c.check_attention(q, k, v, o, ls)
+
+
+def test_masks_of_the_lowest_value():
+    """Scores that overflow to -infinity (a key of the lowest values) weigh nothing; a row whose
+    only key is one attends to it all the same or to nothing, but is never NaN by accident."""
+    c = Case(38, [5, 0], heads=1, dim=64, room=40)
+    q = [np.full((2, 1, 64), 60000, np.float16), np.full((40, 1, 64), 60000, np.float16)]
+    k = [np.full((2, 1, 64), -60000, np.float16), np.full((40, 1, 64), -60000, np.float16)]
+    v = [c.rows(2), c.rows(40)]
+    c.attend(q, k, v, accumulate=True)
+
+
+def test_workspace_contents_do_not_matter():
+    c = Case(39, [2600, 700], heads=1, dim=64, page=64, room=60)
+    for n in ([1, 1], [60, 3]):
+        q, k, v = _scaled(c, n, 1), [c.rows(m) for m in n], [c.rows(m) for m in n]
+        outs = []
+        for fill in (0, 0x7F, 0xFF):
+            size = fq.flex_paged_attention_ws_bytes(c.cache, 1, sum(n), max(n), True)
+            c.cache.weight.zero_()
+            o, ls = c.attend(q, k, v, accumulate=True, check=False,
+                             ws=torch.full((size,), fill, dtype=torch.uint8, device="cuda"))
+            outs.append((o, ls, c.cache.weight.clone()))
+        for x in outs[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(outs[0], x))
