@@ -484,36 +484,47 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 // bytes a slot, and this pass reads them and updates the weights: 12 bytes a slot instead
 // of the codes and their conversion again (32 sequences of 500 to 1999 slots, 32 heads of
 // 64: 72 us with the kernel below).
+template <bool LOOP>
 __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
     pdl_trigger();
     const PagedView& c = A.c;
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
     const int n = rows_of(A.rows, b, first, c.status);
-    const int ctx = slots_of(c, b), held = ctx + (A.fresh != nullptr && A.k_new != nullptr);
-    const int s0 = (blockIdx.x * 128 + threadIdx.x) * 4;      // four slots of one page
-    const bool live = n > 0 && s0 < held, fits = s0 < paged_capacity(c);
-    if (live && !fits) paged_bad(c);                          // no slot for the new token
-    const int p = live && fits ? page_of(c, b, s0) : -1;
-    if (p < 0) {
-        pdl_wait();                                           // (a launch that ends is one whose predecessors have ended)
-        return;
-    }
-    const int64_t row = slot_row(c, p, head, s0);
-    float4 w = *reinterpret_cast<const float4*>(c.weight + row);
-    pdl_wait();                                               // the attention kernel writes what follows
-    const float2 stats = A.stats[static_cast<int64_t>(first) * A.plan.heads + head];
-    const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
-    const float fresh = s0 + 4 > ctx && held > ctx ? prob_of(A.fresh[b * A.plan.heads + head], stats) : 0.f;
-    auto one = [&](float& x, float score, int s) {
-        if (s < ctx) x += prob_of(score, stats);
-        else if (s < held) x = fresh;
+    const int ctx = slots_of(c, b), held = n > 0 ? ctx + (A.k_new != nullptr) : 0, cap = paged_capacity(c);
+    // four slots of one page at a time; their row, -1: none
+    auto find_row = [&](int s0) {
+        if (s0 >= held) return -1;
+        if (s0 >= cap) {
+            paged_bad(c);                                     // no slot for the new token
+            return -1;
+        }
+        const int p = page_of(c, b, s0);
+        return p < 0 ? -1 : slot_row(c, p, head, s0);
     };
-    one(w.x, sc.x, s0);
-    one(w.y, sc.y, s0 + 1);
-    one(w.z, sc.z, s0 + 2);
-    one(w.w, sc.w, s0 + 3);
-    *reinterpret_cast<float4*>(c.weight + row) = w;
+    int s0 = (blockIdx.x * 128 + threadIdx.x) * 4, row = find_row(s0);
+    pdl_wait();                                               // the attention kernel writes what follows
+    if (LOOP ? s0 >= held : row < 0) return;
+    const float2 stats = A.stats[static_cast<int64_t>(first) * A.plan.heads + head];
+    for (;;) {
+        if (!LOOP || row >= 0) {
+            const float fresh = s0 + 4 > ctx && held > ctx ? prob_of(A.fresh[b * A.plan.heads + head], stats) : 0.f;
+            const float4 sc = *reinterpret_cast<const float4*>(A.scores + row);
+            float4 w = *reinterpret_cast<const float4*>(c.weight + row);
+            auto one = [&](float& x, float score, int s) {
+                if (s < ctx) x += prob_of(score, stats);
+                else if (s < held) x = fresh;
+            };
+            one(w.x, sc.x, s0);
+            one(w.y, sc.y, s0 + 1);
+            one(w.z, sc.z, s0 + 2);
+            one(w.w, sc.w, s0 + 3);
+            *reinterpret_cast<float4*>(c.weight + row) = w;
+        }
+        s0 += gridDim.x * 512;
+        if (!LOOP || s0 >= held) break;
+        row = find_row(s0);
+    }
 }
 
 // Any number of rows: the scores again (about 25 of the 67 us of 12 sequences with 1 to 97 new
@@ -521,8 +532,8 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
 // through all query rows of the sequence, so every key's sum stays in its lanes and is added
 // in one fixed order; no atomics. Query rows pass through shared memory, 32 at a time, for 4
 // warps.
-template <int D, int BITS, int GS>
-__global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
+template <int D, int BITS, int GS, bool LOOP>
+__global__ void __launch_bounds__(128, D == 64 ? 7 : 4) paged_weight_kernel(AttnArgs A) {
     const PagedView& c = A.c;
     const RowsPlan& plan = A.plan;
     const __half *q = A.q, *k_new = A.k_new;
@@ -535,139 +546,147 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(AttnArgs A) {
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
     const int n = rows_of(A.rows, b, first, c.status), ctx = slots_of(c, b), cap = paged_capacity(c);
-    const int old_blocks = (ctx + 127) / 128;
-    const bool fresh = static_cast<int>(blockIdx.x) >= old_blocks;
-    const int j0 = (static_cast<int>(blockIdx.x) - (fresh ? old_blocks : 0)) * 128 + warp * 32;    // slot, or fresh token
-    const int jend = fresh ? (k_new ? n : 0) : ctx;
-    if (j0 - warp * 32 >= jend || n == 0) {             // a sequence without new tokens keeps its weights
-        pdl_wait();                                     // (a launch that ends is one whose predecessors have ended)
-        return;
-    }
-    // rows of the tokens that see any of the block's keys
-    const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
-    const int tiles = (row_end - row_lo + QR - 1) / QR;
-    auto load_q = [&](int s) {
-        for (int i = tid; i < QR * (D / 8); i += 128) {
-            const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
-            const bool ok = r < row_end;
-            const int tok = ok ? token_of(plan, r) : 0, h = ok ? head * plan.share + r - tok * plan.share : 0;
-            cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
-        }
-        cp_commit();
-    };
-    auto load_stats = [&](int s) {
-        if (tid < QR) {
-            const int r = row_lo + s * QR + tid;
-            const int tok = token_of(plan, r), h = head * plan.share + r - tok * plan.share;
-            sl[s & 1][tid] = r < row_end ? A.stats[static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h] : make_float2(0.f, 0.f);
-        }
-    };
-    // All that the attention kernel does not write is requested before it is waited for: the
-    // first queries, and the keys, which become operands (in the order of the dims, as the
-    // queries' are) meanwhile.
-    load_q(0);
-    int row[4];                                         // pool rows of keys j0 + g + 8 i, -1: none
-    uint32_t a[2][D / 16][4];
-    const int kgrp = t * (D / 4) / GS;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int j = j0 + g + 8 * i, slot = fresh ? ctx + j : j;
-        row[i] = -1;
-        if (j < jend) {
-            if (slot >= cap) {
-                paged_bad(c);
-            } else {
-                const int p = page_of(c, b, slot);
-                if (p >= 0) row[i] = slot_row(c, p, head, slot);
+    const int old_blocks = (ctx + 127) / 128, blocks = n == 0 ? 0 : old_blocks + (k_new ? (n + 127) / 128 : 0);
+    bool waited = false;
+    for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const bool fresh = block >= old_blocks;
+        const int j0 = (block - (fresh ? old_blocks : 0)) * 128 + warp * 32;     // slot, or fresh token
+        const int jend = fresh ? n : ctx;
+        // rows of the tokens that see any of the block's keys
+        const int row_lo = fresh ? (j0 - warp * 32) * plan.share : 0, row_end = n * plan.share;
+        const int tiles = (row_end - row_lo + QR - 1) / QR;
+        auto load_q = [&](int s) {
+            for (int i = tid; i < QR * (D / 8); i += 128) {
+                const int r = row_lo + s * QR + i / (D / 8), d = (i % (D / 8)) * 8;
+                const bool ok = r < row_end;
+                const int tok = ok ? token_of(plan, r) : 0, h = ok ? head * plan.share + r - tok * plan.share : 0;
+                cp16(smem_addr(&sq[s & 1][(i / (D / 8)) * LD + d]), q + static_cast<int64_t>(first + tok) * q_stride + h * D + d, ok);
             }
-        }
-        uint32_t pr[D / 32][4];
-        if (!fresh) {
-            const int64_t r = row[i] < 0 ? 0 : row[i];
-            const uint32_t meta = row[i] < 0 ? 0u : __ldg(c.km + r * NG + kgrp);
-            const uint32_t step = dup16(step16_of(meta)), mn = dup_lo(meta);
-            const uint8_t* kc = c.kc + r * KB + t * (KB / 4);
-            uint32_t x[KB / 16];
-#pragma unroll
-            for (int w = 0; w < KB / 16; w += 2) {
-                const uint2 v = row[i] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(kc + w * 4));
-                x[w] = v.x;
-                x[w + 1] = v.y;
-            }
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) key_pairs<BITS>(pr[w], x[w * (BITS / 4)], x[w * (BITS / 4) + BITS / 4 - 1], step, mn);
-        } else {
-            const uint4* x = reinterpret_cast<const uint4*>(k_new + static_cast<int64_t>(first + (j < jend ? j : 0)) * kv_stride +
-                                                            head * D + t * (D / 4));
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) key_pairs_fresh<8>(pr[w], j < jend ? __ldg(x + w) : make_uint4(0, 0, 0, 0));
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            // at 4 bits the pairs are (d, d + 4): neighbours again
-            const bool nibbles = BITS == 4 && !fresh;
-            a[i / 2][2 * w][i % 2] = nibbles ? byte_perm(pr[w][0], pr[w][1], 0x5410u) : pr[w][0];
-            a[i / 2][2 * w][2 + i % 2] = nibbles ? byte_perm(pr[w][2], pr[w][3], 0x5410u) : pr[w][1];
-            a[i / 2][2 * w + 1][i % 2] = nibbles ? byte_perm(pr[w][0], pr[w][1], 0x7632u) : pr[w][2];
-            a[i / 2][2 * w + 1][2 + i % 2] = nibbles ? byte_perm(pr[w][2], pr[w][3], 0x7632u) : pr[w][3];
-        }
-    }
-    pdl_wait();
-    load_stats(0);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    // 8 rows and the warp's 32 keys; ALL: every row sees every key
-    auto rows8 = [&](int s, int u, auto all_c) {
-        constexpr bool ALL = decltype(all_c)::value;
-        const int r0 = row_lo + s * QR + u * 8;
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const __half* qr = &sq[s & 1][(u * 8 + g) * LD + t * (D / 4)];
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            const uint4 z = *reinterpret_cast<const uint4*>(qr + w * 8);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                mma168(sc[k], a[k][2 * w], z.x, z.y);
-                mma168(sc[k], a[k][2 * w + 1], z.z, z.w);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = r0 + 2 * t + e;
-            const float2 stats = sl[s & 1][u * 8 + 2 * t + e];
-            // the last key that the row sees; a row behind the last one sees none
-            const int seen = ALL ? 0 : r >= row_end ? -1 : fresh ? token_of(plan, r) : INT32_MAX;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const float p = prob_of(sc[k][2 * hh + e], stats);
-                    if (ALL || j0 + k * 16 + hh * 8 + g <= seen) sum[2 * k + hh] += p;
-                }
-        }
-    };
-    for (int s = 0; s < tiles; ++s) {
-        if (s + 1 < tiles) {
-            load_q(s + 1);
-            load_stats(s + 1);
-        } else {
             cp_commit();
-        }
-        cp_wait<1>();
-        __syncthreads();
-        if (!fresh && row_lo + (s + 1) * QR <= row_end) {
+        };
+        auto load_stats = [&](int s) {
+            if (tid < QR) {
+                const int r = row_lo + s * QR + tid;
+                const int tok = token_of(plan, r), h = head * plan.share + r - tok * plan.share;
+                sl[s & 1][tid] = r < row_end ? A.stats[static_cast<int64_t>(first + tok) * (plan.heads * plan.share) + h] : make_float2(0.f, 0.f);
+            }
+        };
+        // All that the attention kernel does not write is requested before it is waited for: the
+        // first queries, and the keys, which become operands (in the order of the dims, as the
+        // queries' are) meanwhile.
+        load_q(0);
+        int row[4];                                         // pool rows of keys j0 + g + 8 i, -1: none
+        uint32_t a[2][D / 16][4];
+        const int kgrp = t * (D / 4) / GS;
 #pragma unroll
-            for (int u = 0; u < QR / 8; ++u) rows8(s, u, std::true_type{});
-        } else {
-            for (int u = 0; u < QR / 8 && row_lo + s * QR + u * 8 < row_end; ++u) rows8(s, u, std::false_type{});
-        }
-        __syncthreads();
-    }
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + g + 8 * i, slot = fresh ? ctx + j : j;
+            row[i] = -1;
+            if (j < jend) {
+                if (slot >= cap) {
+                    paged_bad(c);
+                } else {
+                    const int p = page_of(c, b, slot);
+                    if (p >= 0) row[i] = slot_row(c, p, head, slot);
+                }
+            }
+            uint32_t pr[D / 32][4];
+            if (!fresh) {
+                const int64_t r = row[i] < 0 ? 0 : row[i];
+                const uint32_t meta = row[i] < 0 ? 0u : __ldg(c.km + r * NG + kgrp);
+                const uint32_t step = dup16(step16_of(meta)), mn = dup_lo(meta);
+                const uint8_t* kc = c.kc + r * KB + t * (KB / 4);
+                uint32_t x[KB / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        if (t == 0 && row[i] >= 0) c.weight[row[i]] = fresh ? sum[i] : c.weight[row[i]] + sum[i];
+                for (int w = 0; w < KB / 16; w += 2) {
+                    const uint2 v = row[i] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(kc + w * 4));
+                    x[w] = v.x;
+                    x[w + 1] = v.y;
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t z[4];
+                    key_pairs<BITS>(z, x[w * (BITS / 4)], x[w * (BITS / 4) + BITS / 4 - 1], step, mn);
+                    // at 4 bits the pairs are (d, d + 4): neighbours again
+                    pr[w][0] = BITS == 4 ? byte_perm(z[0], z[1], 0x5410u) : z[0];
+                    pr[w][1] = BITS == 4 ? byte_perm(z[2], z[3], 0x5410u) : z[1];
+                    pr[w][2] = BITS == 4 ? byte_perm(z[0], z[1], 0x7632u) : z[2];
+                    pr[w][3] = BITS == 4 ? byte_perm(z[2], z[3], 0x7632u) : z[3];
+                }
+            } else {
+                const uint4* x = reinterpret_cast<const uint4*>(k_new + static_cast<int64_t>(first + (j < jend ? j : 0)) * kv_stride +
+                                                                head * D + t * (D / 4));
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) key_pairs_fresh<8>(pr[w], j < jend ? __ldg(x + w) : make_uint4(0, 0, 0, 0));
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                a[i / 2][2 * w][i % 2] = pr[w][0];
+                a[i / 2][2 * w][2 + i % 2] = pr[w][1];
+                a[i / 2][2 * w + 1][i % 2] = pr[w][2];
+                a[i / 2][2 * w + 1][2 + i % 2] = pr[w][3];
+            }
+        }
+        if (!waited) pdl_wait();
+        waited = true;
+        load_stats(0);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // 8 rows and the warp's 32 keys; ALL: every row sees every key
+        auto rows8 = [&](int s, int u, auto all_c) {
+            constexpr bool ALL = decltype(all_c)::value;
+            const int r0 = row_lo + s * QR + u * 8;
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const __half* qr = &sq[s & 1][(u * 8 + g) * LD + t * (D / 4)];
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                const uint4 z = *reinterpret_cast<const uint4*>(qr + w * 8);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mma168(sc[k], a[k][2 * w], z.x, z.y);
+                    mma168(sc[k], a[k][2 * w + 1], z.z, z.w);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 2 * t + e;
+                const float2 stats = sl[s & 1][u * 8 + 2 * t + e];
+                // the last key that the row sees; a row behind the last one sees none
+                const int seen = ALL ? 0 : r >= row_end ? -1 : fresh ? token_of(plan, r) : INT32_MAX;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const float p = prob_of(sc[k][2 * hh + e], stats);
+                        if (ALL || j0 + k * 16 + hh * 8 + g <= seen) sum[2 * k + hh] += p;
+                    }
+            }
+        };
+        for (int s = 0; s < tiles; ++s) {
+            if (s + 1 < tiles) {
+                load_q(s + 1);
+                load_stats(s + 1);
+            } else {
+                cp_commit();
+            }
+            cp_wait<1>();
+            __syncthreads();
+            if (!fresh && row_lo + (s + 1) * QR <= row_end) {
+#pragma unroll
+                for (int u = 0; u < QR / 8; ++u) rows8(s, u, std::true_type{});
+            } else {
+                for (int u = 0; u < QR / 8 && row_lo + s * QR + u * 8 < row_end; ++u) rows8(s, u, std::false_type{});
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+            if (t == 0 && row[i] >= 0) c.weight[row[i]] = fresh ? sum[i] : c.weight[row[i]] + sum[i];
+        }
+        if (!LOOP) break;
     }
+    if (!waited) pdl_wait();        // (a launch that ends is one whose predecessors have ended)
 }
 
 // ---- host -----------------------------------------------------------------------------------
@@ -679,6 +698,20 @@ struct AttnPlan {
 };
 
 inline int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Blocks along a sequence's keys of the weights' kernels. A table may be far longer than what its
+// sequences hold: above 256 blocks a multiprocessor no more are launched than fill the
+// device twice, and each goes on to the keys that are left (LOOP). Below, a block for
+// every piece: the loop's registers cost 2 of the ragged chunks' 70 us.
+struct WeightGrid {
+    dim3 grid;
+    bool loop;
+};
+WeightGrid weight_grid(int64_t most, int heads, int batch) {
+    const int64_t pairs = static_cast<int64_t>(heads) * batch, fill = (32LL * sm_count() + pairs - 1) / pairs;
+    const bool loop = most > fill && most * pairs > 256LL * sm_count();
+    return WeightGrid{dim3(static_cast<unsigned>(loop ? fill : most), heads, batch), loop};
+}
 
 AttnPlan attn_plan(const flex_paged_cache* c, int n_heads, int batch, int total, int most, bool accumulate) {
     AttnPlan p{};
@@ -806,12 +839,19 @@ extern "C" int flex_paged_attention(const flex_paged_cache* cache, const void* q
     }
     if (a.scores != nullptr) {
         const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
-        launch_k(paged_weight_one_kernel, dim3(static_cast<unsigned>((cap + (k_new ? 1 : 0) + 511) / 512), kvh, batch), dim3(128), 0, st, true, a);
+        const WeightGrid w = weight_grid((cap + (k_new ? 1 : 0) + 511) / 512, kvh, batch);        // every 512 slots
+        if (w.loop)
+            launch_k(paged_weight_one_kernel<true>, w.grid, dim3(128), 0, st, true, a);
+        else
+            launch_k(paged_weight_one_kernel<false>, w.grid, dim3(128), 0, st, true, a);
     } else if (accumulate) {
         const int64_t cap = static_cast<int64_t>(cache->max_pages) * cache->page_size;
-        // every 128 slots, and 128 fresh tokens; blocks behind a sequence's end return at once
-        const dim3 wgrid(static_cast<unsigned>((cap + 127) / 128 + (k_new ? (most + 127) / 128 : 0)), kvh, batch);
-#define WEIGHT(D_, B_, G_) launch_k(paged_weight_kernel<D_, B_, G_>, wgrid, dim3(128), 0, st, true, a)
+        const WeightGrid w = weight_grid((cap + 127) / 128 + (k_new ? (most + 127) / 128 : 0), kvh, batch);      // every 128 keys
+#define WEIGHT(D_, B_, G_)                                                                              \
+    do {                                                                                                \
+        if (w.loop) launch_k(paged_weight_kernel<D_, B_, G_, true>, w.grid, dim3(128), 0, st, true, a); \
+        else launch_k(paged_weight_kernel<D_, B_, G_, false>, w.grid, dim3(128), 0, st, true, a);       \
+    } while (0)
         if (D == 64) {
             if (B == 4 && G == 32) WEIGHT(64, 4, 32); else if (B == 4) WEIGHT(64, 4, 64);
             else if (G == 32) WEIGHT(64, 8, 32); else WEIGHT(64, 8, 64);

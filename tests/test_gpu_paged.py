@@ -702,3 +702,17 @@ def test_workspace_contents_do_not_matter():
             outs.append((o, ls, c.cache.weight.clone()))
         for x in outs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(outs[0], x))
+
+
+@pytest.mark.parametrize("most", [1, 5])
+def test_tables_far_longer_than_the_sequences(most):
+    """The weights' pass over a table of a million slots a sequence, of which few are held."""
+    c = Case(40, [300, 20, 130], heads=6, dim=64, page=1024, room=most)
+    wide = torch.full((3, 1 << 10), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.cache.page_table.shape[1]] = c.cache.page_table
+    c.cache.page_table, c.cache.max_pages = wide, 1 << 10
+    n = [most, 1, most]
+    for _ in range(2):
+        c.attend(_scaled(c, n, 12), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
+    one = [1, 1, 1]
+    c.attend(_scaled(c, one, 6), [c.rows(1)] * 3, [c.rows(1)] * 3, accumulate=True)
