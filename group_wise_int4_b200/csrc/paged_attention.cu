@@ -183,9 +183,8 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     }
 
     // Scores of T tiles of 16 keys (-inf where hidden) -> running maximum, sum, and the
-    // probabilities as the value product's operand. The maximum moves only when a score
-    // passes it so far that its weight would pass 2^8: until then probabilities are up to 256, with the same
-    // relative error, and nothing is rescaled.
+    // probabilities as the value product's operand. The maximum moves only when a score passes it
+    // by kSlack: until then nothing is rescaled.
     auto softmax = [&](auto& sc, auto& pb, auto tiles_c) {
         constexpr int T = decltype(tiles_c)::value;
 #pragma unroll
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
             for (int k = 0; k < T; ++k) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(exponent_of(sc[k][n][e], m[n][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(sc[k][n][e] - m[n][e & 1], kLog2e, kLift));
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];
                 pb[k][n][0] = mat_trans(half2_of(p[0], p[1]));
@@ -464,14 +463,15 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 4)
                     *reinterpret_cast<uint4*>(A.o + at * D + g * (D / 8) + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                if (g == 0) put_stats(A, at, m[n][e], sum);
+                if (g == 0) put_stats(A, at, m[n][e], sum, kLift);
             } else if (u.slot < A.slots) {
+                const float down = 0.015625f;                  // 2^-kLift
                 float* p = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + r) * (D + 4);
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 2)
                     *reinterpret_cast<float4*>(p + g * (D / 8) + 2 * i) =
-                        make_float4(acc[i][n][e], acc[i][n][2 + e], acc[i + 1][n][e], acc[i + 1][n][2 + e]);
-                if (g == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[n][e], sum);
+                        make_float4(acc[i][n][e] * down, acc[i][n][2 + e] * down, acc[i + 1][n][e] * down, acc[i + 1][n][2 + e] * down);
+                if (g == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[n][e], sum * down);
             }
         }
 }

@@ -271,7 +271,10 @@ struct AttnArgs {
 // Exponent (base 2) of a score's weight relative to m. The difference comes first: it is exact
 // near the maximum and 0 at it, however large the scores are.
 __device__ __forceinline__ float exponent_of(float score, float m) { return (score - m) * kLog2e; }
-constexpr float kSlack = 8.f * kLn2;                // a maximum may be passed so far: weights up to 2^8
+// Weights are 2^kLift times exp(score - m), and the maximum m may be passed by kSlack: up to 2^14,
+// which fp16 holds, as it does in full precision what is 2^-20 of them (without the
+// lift weights below 2^-14 would be subnormal, and lose bits, in long histories).
+constexpr float kLift = 6.f, kSlack = 8.f * kLn2;
 
 // A row's statistics, at [row][head]: sum = 2^left times the sum of exp(score - top).
 __device__ __forceinline__ void put_stats(const AttnArgs& A, int64_t at, float top, float sum, float left = 0.f) {

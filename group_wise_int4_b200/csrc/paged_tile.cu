@@ -24,9 +24,9 @@
 // unit is busy 1024. Tried and slower: the two tiles' exponentials in turns (1040), a
 // quarter of them as polynomials (1125), two threads a row.
 //
-// The running maximum m only moves when a score passes it so far that its weight would pass
-// 2^8: until then the probabilities are up to 256 instead of 1, which fp16 holds with
-// the same relative error, and O is not rescaled. The final quotient does not depend on m.
+// The running maximum m only moves when a score passes it by kSlack: until then the weights grow
+// instead of O being rescaled (fp16 holds them with the same relative error). The final
+// quotient does not depend on m.
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -86,13 +86,14 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t base, int r, int c) {
     return base + (c >> 3) * (ROWS * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16;
 }
 
-// Exponents are score * log2 e - fl(m log2 e), one fused multiply-add for each score: against
-// (score - m) log2 e every weight of the row is 2^leftover(m) times as large. A maximum of
-// 2^23 or more would leave factors that overflow: such rows' scores have m subtracted in
-// tensor memory first, and no shift.
+// Exponents are score * log2 e + shift_of(m), one fused multiply-add for each score, so that
+// weights are 2^lift_of(m) times exp(score - m): kLift but for what rounding the shift left. A
+// maximum of 2^23 or more would leave factors that overflow: such rows' scores have m
+// subtracted in tensor memory first.
 __device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= 8388608.f && m != -FLT_MAX; }
-__device__ __forceinline__ float leftover(float m) {
-    return m == -FLT_MAX || is_big(m) ? 0.f : fmaf(m, kLog2e, -__fmul_rn(m, kLog2e));
+__device__ __forceinline__ float shift_of(float m) { return is_big(m) ? kLift : kLift - __fmul_rn(m, kLog2e); }
+__device__ __forceinline__ float lift_of(float m) {
+    return m == -FLT_MAX || is_big(m) ? kLift : fmaf(m, kLog2e, shift_of(m));
 }
 
 template <int D, int BITS, int GS, int TILES>
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     if (__any_sync(0xffffffffu, top > limit)) {
                         const bool moves = top > m + kSlack;    // a row's result depends on no other row
-                        const float was = m, left = leftover(m);
+                        const float was = m, lift = lift_of(m);
                         m = moves ? top : m;
-                        const float f = moves ? exp2_fast(fmaf(was - m, kLog2e, leftover(m) - left)) : 1.f;
+                        const float f = moves ? exp2_fast(fmaf(was - m, kLog2e, lift_of(m) - lift)) : 1.f;
                         l = f32x2_scale(l, f);
                         limit = is_big(m) ? -INFINITY : m + kSlack;
-                        shift = is_big(m) ? 0.f : -__fmul_rn(m, kLog2e);
+                        shift = shift_of(m);
                         if (j > 0 && __any_sync(0xffffffffu, moves)) {
                             if (!(ok = wait(o_done + 16 * tile + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1))) return;
                             tc::fence_after_sync();
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                             }
                         }
                         if (__any_sync(0xffffffffu, is_big(m))) {
-                            // S becomes S - m, and its shift is 0
+                            // S becomes S - m
 #pragma unroll 1
                             for (int i = 0; i < NK; i += 16) {
                                 uint32_t y[16];
@@ -289,8 +290,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         f32x2_get(l, l0, sum);
         sum += l0;
         if (ok) {
-            // sum and O hold 2^leftover(m) times the weights relative to m; the quotient does not
-            const float inv = sum == 0.f ? 0.f : 1.f / sum, even = exp2_fast(-leftover(m));
+            // partial results are relative to m itself
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, even = exp2_fast(-lift_of(m));
             const int64_t at = static_cast<int64_t>(u.first + token) * (A.plan.heads * share) + h;
             float* part = A.parts + ((static_cast<int64_t>(u.slot) * A.plan.heads + head) * R + tile * 128 + r) * (D + 4);
             const bool wild = wild_flag != 0;
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 if (u.parts > 1) {
                     if (u.slot < A.slots) *reinterpret_cast<float2*>(part + D) = make_float2(m, sum * even);
                 } else {
-                    put_stats(A, at, m, sum, leftover(m));
+                    put_stats(A, at, m, sum, lift_of(m));
                 }
             }
         }
