@@ -26,9 +26,9 @@ namespace {
 // its scales into steps once, for all lanes that use them.
 //
 // Three instructions for two values (extract, subtract the exponent's offset, one fused
-// multiply-add) make about 220 of the 430 that 16 keys of 128 dims take at 4 bits, so the
+// multiply-add) make about 220 of the 450 that 16 keys of 128 dims take at 4 bits, so the
 // issue slots bound it, not the memory: 144 sequences of 512 to 543 slots at 96 heads take
-// 300 us (3.5 TB/s, 54% of the measured copy bandwidth, 69% of the issue slots); 8-bit
+// 307 us (3.5 TB/s, 53% of the measured copy bandwidth, 66% of the issue slots); 8-bit
 // codes of four sequences of 3001 to 60001 slots shared by 8 heads each 65 us (75%).
 // Warps of a multiprocessor, by registers: without spilling the kernel takes 168 at 8 rows of 128
 // dims (16 warps of 128 registers spill, and take 440 us instead of 338 for a decode step of
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
     }
 }
 
-// Any number of rows: the scores again (about 25 of the 67 us of 12 sequences with 1 to 97 new
+// Any number of rows: the scores again (about 25 of the 71 us of 12 sequences with 1 to 97 new
 // tokens over up to 1500 slots, 32 heads of 64: latency of the first loads, then issue slots). A warp holds 32 keys as operands in registers and goes
 // through all query rows of the sequence, so every key's sum stays in its lanes and is added
 // in one fixed order; no atomics. Query rows pass through shared memory, 32 at a time, for 4

@@ -19,7 +19,8 @@
 // (wait, S, softmax, P V in turn): 5100 cycles per 128 keys and 256 rows. One warp that
 // issues all products: 1745 us for 2000 tokens over 8 and 16 thousand slots at 32 heads of
 // 128, one a tile 1169, one for each kind and tile 1018, with the stages' release off its
-// path to the next scores 966 us: 0.90 PFLOP/s, 54% of the measured fp16 rate. What bounds
+// path to the next scores 966 us, scores of any magnitude 986: 0.88 PFLOP/s, 53% of the
+// measured fp16 rate. What bounds
 // it now is the softmax warps: 2080 cycles a block of 64 keys, of which the exponential
 // unit is busy 1024. Tried and slower: the two tiles' exponentials in turns (1040), a
 // quarter of them as polynomials (1125), two threads a row.
