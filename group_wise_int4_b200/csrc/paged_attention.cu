@@ -3,9 +3,9 @@
 // For row r (token i of sequence b, query head h, key head g = h / share):
 //   s_j = q_r . k_j over the slots j < ctx_len[b] and the fresh tokens 0..i,
 //   lse_r = log sum_j exp(s_j),  o_r = sum_j exp(s_j - lse_r) v_j,
-// in one pass over the keys with a running maximum and sum; statistics are fp32,
-// probabilities are rounded to fp16 once, as operands of the
-// value product: at most 2^-11 of each, far below o's own fp16 rounding after the sum.
+// in one pass over the keys with a running maximum and sum; statistics are fp32. Probabilities
+// are fp16 operands of the value product: rounding them costs o about as much as its own
+// rounding does, which up to 4 rows is avoided (TWICE below).
 // k_j and v_j are the fp16 values of paged.cuh, so the products are exact and summed in fp32.
 #include <type_traits>
 

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
                 uint32_t y[32];
+                __syncwarp();                                    // rows that are not there have gone ahead
                 if (nb > 0) {
                     tc::tmem_ld32(to + i, y);
                     tc::tmem_wait_ld(y);
