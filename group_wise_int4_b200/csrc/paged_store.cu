@@ -37,17 +37,56 @@ struct SlotRows {
     }
 };
 
+// Which tokens a block has. search == 0: sequence blockIdx.z, tokens from blockIdx.x * TOKENS on.
+// Otherwise `search` sequences of very unequal lengths have their pieces one after the other
+// along blockIdx.x, and every warp finds its block's by counting (one long prompt among single tokens
+// would leave nearly all blocks of a rectangle empty).
+struct Span {
+    int b, first, n, t0;
+};
+template <int TOKENS>
+__device__ __forceinline__ Span find_span(const RowsOf& rows, int search, int* status) {
+    Span s{static_cast<int>(blockIdx.z), 0, 0, static_cast<int>(blockIdx.x) * TOKENS};
+    if (search == 0) {
+        s.n = rows_of(rows, s.b, s.first, status);
+        return s;
+    }
+    const int lane = threadIdx.x & 31;
+    int left = blockIdx.x;                          // pieces still to pass
+    for (int b0 = 0; b0 < search; b0 += 32) {
+        int first = 0, n = 0;
+        if (b0 + lane < search) n = rows_of(rows, b0 + lane, first, status);
+        const int pieces = (n + TOKENS - 1) / TOKENS;           // at most 2^24
+        const int sum = __reduce_add_sync(0xffffffffu, pieces);
+        if (left >= sum) {
+            left -= sum;
+            continue;
+        }
+        int x = pieces;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const int l = __ffs(__ballot_sync(0xffffffffu, left < x)) - 1;
+        s.b = b0 + l;
+        s.first = __shfl_sync(0xffffffffu, first, l);
+        s.n = __shfl_sync(0xffffffffu, n, l);
+        s.t0 = (left - __shfl_sync(0xffffffffu, x - pieces, l)) * TOKENS;
+        return s;
+    }
+    return s;                                       // n = 0: nothing
+}
+
 template <int D, int BITS, int GS, int TOKENS>
 __global__ void __launch_bounds__(PS_THREADS) paged_store_kernel(PagedView c, RowsOf rows, const __half* __restrict__ k_new,
                                                                  const __half* __restrict__ v_new, int64_t row_stride,
-                                                                 const int32_t* __restrict__ pos0) {
+                                                                 const int32_t* __restrict__ pos0, int search) {
     constexpr int L = GS / 16, V = D / 16, KB = D * BITS / 8, NG = D / GS;      // lanes of a group, threads of a head
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.z;
-    int first;
-    const int n = rows_of(rows, b, first, c.status);
-    const int t0 = blockIdx.x * TOKENS;
+    const Span span = find_span<TOKENS>(rows, search, c.status);
+    const int b = span.b, first = span.first, n = span.n, t0 = span.t0;
     if (t0 >= n) return;
     const int vecs = c.heads * V;                   // threads of one row's keys
     const int col = blockIdx.y * PS_THREADS + threadIdx.x;
@@ -97,14 +136,12 @@ __global__ void __launch_bounds__(PS_THREADS) paged_store_kernel(PagedView c, Ro
 template <int D, int BITS, int GS, int TOKENS>
 __global__ void __launch_bounds__(PS_THREADS) paged_load_kernel(PagedView c, RowsOf rows, __half* __restrict__ k_out,
                                                                 __half* __restrict__ v_out, int64_t row_stride,
-                                                                const int32_t* __restrict__ from) {
+                                                                const int32_t* __restrict__ from, int search) {
     constexpr int V = D / 16, KB = D * BITS / 8, NG = D / GS;
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.z;
-    int first;
-    const int n = rows_of(rows, b, first, c.status);
-    const int t0 = blockIdx.x * TOKENS;
+    const Span span = find_span<TOKENS>(rows, search, c.status);
+    const int b = span.b, first = span.first, n = span.n, t0 = span.t0;
     if (t0 >= n) return;
     const int vecs = c.heads * V;
     const int col = blockIdx.y * PS_THREADS + threadIdx.x;
@@ -220,9 +257,18 @@ int validate_kv_rows(const flex_paged_cache* c, const void* k, const void* v, in
     return FLEX_OK;
 }
 
-inline dim3 paged_copy_grid(const flex_paged_cache* c, int batch, int most, int tokens) {
+// A rectangle of the longest sequence's pieces times the batch, or (search) the pieces alone: at
+// most total / tokens + batch. Searching costs a block half a microsecond or more.
+struct CopyGrid {
+    dim3 grid;
+    int search;
+};
+inline CopyGrid paged_copy_grid(const flex_paged_cache* c, int batch, int total, int most, int tokens) {
     const int64_t vecs = 2LL * c->n_kv_heads * c->head_dim / 16;
-    return dim3((most + tokens - 1) / tokens, static_cast<unsigned>((vecs + PS_THREADS - 1) / PS_THREADS), batch);
+    const unsigned y = static_cast<unsigned>((vecs + PS_THREADS - 1) / PS_THREADS);
+    const int64_t wide = (most + tokens - 1) / tokens, pieces = total / tokens + batch;
+    if (wide * batch > 4 * pieces) return CopyGrid{dim3(static_cast<unsigned>(pieces), y, 1), batch};
+    return CopyGrid{dim3(static_cast<unsigned>(wide), y, batch), 0};
 }
 
 }  // namespace
@@ -235,7 +281,8 @@ using namespace flexq;
     do {                                                                                                            \
         const int D = cache->head_dim, B = cache->cfg.num_bits, G = cache->cfg.group_size;                          \
         const cudaStream_t st = as_stream(stream);                                                                  \
-        const dim3 grid = paged_copy_grid(cache, batch, most, most == 1 ? 1 : 4), block(PS_THREADS);                \
+        const CopyGrid g = paged_copy_grid(cache, batch, total, most, most == 1 ? 1 : 4);                           \
+        const dim3 block(PS_THREADS);                                                                               \
         if (D == 64) {                                                                                              \
             if (B == 4 && G == 32) PAGED_RUN(KERNEL, 64, 4, 32, __VA_ARGS__);                                       \
             else if (B == 4) PAGED_RUN(KERNEL, 64, 4, 64, __VA_ARGS__);                                             \
@@ -251,8 +298,8 @@ using namespace flexq;
     } while (0)
 #define PAGED_RUN(KERNEL, D_, B_, G_, ...)                                            \
     do {                                                                              \
-        if (most == 1) launch_k(KERNEL<D_, B_, G_, 1>, grid, block, 0, st, true, __VA_ARGS__); \
-        else launch_k(KERNEL<D_, B_, G_, 4>, grid, block, 0, st, true, __VA_ARGS__);  \
+        if (most == 1) launch_k(KERNEL<D_, B_, G_, 1>, g.grid, block, 0, st, true, __VA_ARGS__, g.search); \
+        else launch_k(KERNEL<D_, B_, G_, 4>, g.grid, block, 0, st, true, __VA_ARGS__, g.search);  \
     } while (0)
 
 extern "C" int flex_paged_store_kv(const flex_paged_cache* cache, const void* k_new, const void* v_new, int64_t row_stride,

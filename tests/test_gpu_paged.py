@@ -716,3 +716,27 @@ def test_tables_far_longer_than_the_sequences(most):
         c.attend(_scaled(c, n, 12), [c.rows(m) for m in n], [c.rows(m) for m in n], accumulate=True)
     one = [1, 1, 1]
     c.attend(_scaled(c, one, 6), [c.rows(1)] * 3, [c.rows(1)] * 3, accumulate=True)
+
+
+@pytest.mark.parametrize("bits,dim", [(4, 64), (8, 128)])
+def test_one_long_prompt_among_single_tokens(bits, dim):
+    """Store and load of a batch of 50 sequences of which one has nearly all rows."""
+    n = [1 if i % 7 else 0 for i in range(50)]
+    n[41] = 333
+    c = Case(41, [(3 * i) % 20 for i in range(50)], heads=2, dim=dim, bits=bits, room=333)
+    k, v = [c.rows(m) for m in n], [c.rows(m) for m in n]
+    start = c.ref.ctx.copy()
+    c.store(k, v, advance=True)
+    sync_status()
+    c.check_slots("added")
+    outs = [torch.full((sum(n) + TAIL, 2 * dim), 5.0, dtype=torch.float16, device="cuda") for _ in "kv"]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+    fq.flex_paged_load_kv(c.cache, outs[0], outs[1], 2 * dim, cu, max(n), total=sum(n),
+                          start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+    sync_status()
+    at = 0
+    for b in range(50):
+        for x, ref in zip(outs, c.ref.load(b, int(start[b]), n[b])):
+            assert np.array_equal(to_np(x[at:at + n[b]]).reshape(n[b], 2, dim).view(np.uint16), ref.view(np.uint16)), b
+        at += n[b]
+    assert all(bool((x[at:] == 5).all()) for x in outs)
