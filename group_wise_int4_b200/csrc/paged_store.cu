@@ -258,7 +258,9 @@ int validate_kv_rows(const flex_paged_cache* c, const void* k, const void* v, in
 }
 
 // A rectangle of the longest sequence's pieces times the batch, or (search) the pieces alone: at
-// most total / tokens + batch. Searching costs a block half a microsecond or more.
+// most total / tokens + batch. us for the rectangle / the
+// pieces, storing at 96 heads of 128: 1024 tokens and 143 single ones 241 / 21, four of 300 to
+// 1024 tokens 33.9 / 35.0, 20 of 200 47.2 / 51.3.
 struct CopyGrid {
     dim3 grid;
     int search;
