@@ -698,7 +698,8 @@ def flex_abi_layout(which: int, field: int) -> int:
 
 
 def flex_set_wait_limit_ns(ns: int) -> int:
-    """Limit of the GEMM's pipeline waits for later launches (0 = default 2 s); returns the old one."""
+    """Limit of the pipeline waits of the GEMM and of the paged attention's tensor-core tiles for later
+    launches (0 = default 2 s); returns the old one."""
     return int(lib().flex_set_wait_limit_ns(int(ns)))
 
 
@@ -721,8 +722,9 @@ def flex_set_gemm_gemv(enable: bool) -> bool:
 
 
 def flex_set_gemm_gate(gate) -> int:
-    """Gate of the tensor-core GEMM's weight loads for later launches (a device int32
-    tensor, or None to remove it); returns the previous gate's address (0 if none)."""
+    """Gate of the tensor-core GEMM's weight loads, and of the value loads of the paged attention's
+    tensor-core tiles, for later launches (a device int32 tensor, or None to remove it);
+    returns the previous gate's address (0 if none)."""
     prev = lib().flex_set_gemm_gate(None if gate is None else _ptr(gate))
     return int(prev or 0)
 

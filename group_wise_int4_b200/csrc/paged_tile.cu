@@ -99,11 +99,11 @@ __device__ __forceinline__ float lift_of(float m) {
 
 template <int D, int BITS, int GS, int TILES>
 __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 : 1)
-    paged_tile_kernel(AttnArgs A, uint64_t wait_ns) {
+    paged_tile_kernel(AttnArgs A, uint64_t wait_ns, const volatile int* gate) {
     using T = TileShape<D, TILES>;
     constexpr int ST = T::ST, KB = D * BITS / 8, NG = D / GS, R = TILES * 128, NX = KB / 16, SOFT = T::SOFT;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t bars[4 * ST + 1 + 8 * TILES];
+    __shared__ __align__(8) uint64_t bars[4 * ST + 1 + 6 * TILES];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, wild_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -127,8 +127,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
 
     const uint32_t bar0 = tc::smem_u32(bars);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
-                   q_full = v_empty + 8 * ST, s_full = q_full + 8, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
-                   drain = o_done + 16 * TILES;
+                   q_full = v_empty + 8 * ST, s_full = q_full + 8, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES;
     const uint32_t sq = (tc::smem_u32(raw) + 1023u) & ~1023u, sk = sq + TILES * T::QB, sv = sk + ST * T::BLOCK;
     volatile int* abort = &abort_flag;
     int* const status = c.status;
@@ -150,7 +149,6 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 tc::bar_init(o_done + 16 * t + 8 * i, 1);
             }
         }
-        for (int i = 0; i < 2 * TILES; ++i) tc::bar_init(drain + 8 * i, 1);
         tc::bar_fence_init();
         abort_flag = 0;
         wild_flag = 0;
@@ -282,7 +280,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                 tc::fence_before_sync();
                 arrive(p_full + 16 * tile + 8 * (j & 1));
             }
-            // (both: no arrival of a commit is still to come when the block's shared memory is given up)
+            // (both: the values' products are whole)
             if (ok && nb > 1) ok = wait(o_done + 16 * tile + 8 * (nb & 1), ((nb - 2) >> 1) & 1);
             if (ok && nb > 0) ok = wait(o_done + 16 * tile + 8 * ((nb - 1) & 1), ((nb - 1) >> 1) & 1);
             tc::fence_after_sync();
@@ -401,6 +399,8 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
             tc::fence_proxy_async_smem();
             arrive(full + 8 * (j % ST));
         };
+        // (flex_set_gemm_gate: the values are held back, so that the scores are on their way meanwhile)
+        if (second && gate != nullptr) ok = __all_sync(0xffffffffu, tc::gate_wait(gate, abort, status, wait_ns));
         uint4 x[2][NX];
         uint32_t meta[2][NG];
         const int page0 = find_page(0);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         const bool value = (warp - SOFT - 4) & 1;
         const uint32_t leader = lane == 0, td = tmem + t * 128;
         bool ok = true;
-        uint32_t last_bar = 0, last_phase = 0;                  // of the last commit
+        int issued = 0;                                         // blocks of keys committed; buffer j & 1 has the j-th
         auto wait1 = [&](uint32_t bar, uint32_t parity) {
             ok = ok && wait(bar, parity);
             return ok;
@@ -467,8 +467,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     tc::mma_f16_if(leader, td + h * NK, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                    b + (((k >> 2) * (NK * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
                 tc::mma_commit_if(leader, s_full + 16 * t + 8 * h);
-                last_bar = s_full + 16 * t + 8 * h;
-                last_phase = (j >> 1) & 1;
+                issued = j + 1;
                 if (j > 1 && j - 2 + ST < nb) {                 // (P V)_(j-2) has read its values
                     arrive(v_empty + 8 * ((j - 2) % ST));
                     if (ST > 2) arrive(k_empty + 8 * ((j - 2) % ST));
@@ -487,18 +486,18 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
                     tc::mma_f16_ts_if(leader, tmem + TILES * 128 + t * D, td + h * NK + k * 8, b + k * (2048 >> 4), idesc,
                                       j > 0 || k > 0);
                 tc::mma_commit_if(leader, o_done + 16 * t + 8 * h);
-                last_bar = o_done + 16 * t + 8 * h;
-                last_phase = (j >> 1) & 1;
+                issued = j + 1;
             }
         }
-        if (!ok) {                                              // what was issued reads shared memory: let it end
-            volatile int never = 0;
-            const uint32_t bar = drain + 8 * (warp - SOFT - 4);
-            tc::mma_commit_if(leader, bar);
-            tc::bar_wait(bar, 0, &never, status, wait_ns);
-            if (last_bar != 0) tc::bar_wait(last_bar, last_phase, &never, status, wait_ns);
-            __syncwarp();
-        }
+        // What was issued (each time with a commit) reads shared memory, writes tensor memory and
+        // arrives at barriers: it ends before the block does, whoever has given up. (This warp may
+        // have issued its last products and be content while the softmax warps no longer wait
+        // for them.) Not with the caller's limit, which may be the one that ran out.
+        volatile int never = 0;
+        const uint32_t done = (value ? o_done : s_full) + 16 * t;
+        for (int j = max(0, issued - 2); j < issued; ++j)
+            tc::bar_wait(done + 8 * (j & 1), (j >> 1) & 1, &never, status, tc::kWaitLimitNs);
+        __syncwarp();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -514,7 +513,7 @@ void launch_one(const AttnArgs& a, int64_t units, cudaStream_t st) {
     using T = TileShape<D, TILES>;
     set_smem_once(paged_tile_kernel<D, BITS, GS, TILES>, T::SMEM);
     launch_k(paged_tile_kernel<D, BITS, GS, TILES>, dim3(static_cast<unsigned>(units * a.plan.heads)), dim3(T::THREADS),
-             T::SMEM, st, true, a, pipeline_wait_ns());
+             T::SMEM, st, true, a, pipeline_wait_ns(), reinterpret_cast<const volatile int*>(gemm_gate()));
     launch_join<D, 128 * TILES, 128, kTileMin>(a, st);
 }
 

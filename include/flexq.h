@@ -434,8 +434,8 @@ int flex_paged_evict(const flex_paged_cache* cache, int32_t budget, int32_t rece
 int flex_get_status(void* stream);
 
 /* Failure detection: limit, in nanoseconds, after which a wait inside the pipeline of
- * the tensor-core GEMM kernel (operand stages, dequantised tiles, MMA completion) gives
- * up. The kernel then records FLEX_ERR_TIMEOUT (read by flex_get_status), stops, lets
+ * the tensor-core GEMM kernel or of the paged attention's tensor-core tiles (operand
+ * stages, dequantised tiles, MMA completion) gives up. The kernel then records FLEX_ERR_TIMEOUT (read by flex_get_status), stops, lets
  * every copy and MMA it issued finish (those drain waits keep the default limit), and
  * exits; its outputs are unspecified, and the device stays usable. Applies to kernels
  * launched after the call (a captured CUDA graph keeps the limit of its capture time);
@@ -443,7 +443,9 @@ int flex_get_status(void* stream);
 uint64_t flex_set_wait_limit_ns(uint64_t ns);
 
 /* Failure-detection test hook: while `gate` is not NULL, every tensor-core GEMM launched
- * waits, before its first weight load, until the device int32 *gate is non-zero. The
+ * waits, before its first weight load, and every tensor-core tile of a paged attention
+ * (more than 32 rows a sequence and key head), before its first value load, until the
+ * device int32 *gate is non-zero. The
  * wait has the limit of flex_set_wait_limit_ns; when it runs out the kernel takes the
  * timeout path described above. A flag that nothing sets thus makes that path run
  * without breaking any kernel. Process-wide; returns the previous gate. gate must stay
