@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedView& c = A.c;
     pdl_wait();
-    pdl_trigger();
     const int head = blockIdx.x % A.plan.heads;
     const Unit u = find_unit<R, 128, kTileMin, 2, true>(c, A.rows, A.plan, blockIdx.x / A.plan.heads);
     if (warp == 0) record_split<R, 128>(A, u, blockIdx.x / A.plan.heads, head);
@@ -160,6 +159,10 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    // Dependents may start from here on, not earlier: a GEMM allocates all tensor memory of a
+    // multiprocessor before it waits for this kernel, and a block that had signalled without
+    // having its own would wait for that GEMM's end, which waits for the block's.
+    pdl_trigger();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     // a warp's threads wait and arrive as one: an abort leaves no part of it behind

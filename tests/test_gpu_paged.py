@@ -740,3 +740,28 @@ def test_one_long_prompt_among_single_tokens(bits, dim):
             assert np.array_equal(to_np(x[at:at + n[b]]).reshape(n[b], 2, dim).view(np.uint16), ref.view(np.uint16)), b
         at += n[b]
     assert all(bool((x[at:] == 5).all()) for x in outs)
+
+
+@pytest.mark.parametrize("most", [60, 200])
+def test_a_gemm_right_behind_the_tiles(most):
+    """The output projection after a chunk's attention, launch after launch without a pause: the
+    GEMM's early blocks and the tiles share the multiprocessors' tensor memory."""
+    c = Case(42, [700, 0, 90], heads=4, dim=64, page=64, room=most)
+    n = [most, 3, most // 2]
+    q, k, v = _scaled(c, n, 8), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    want = c.attend(q, k, v)[0]
+    qd, cu, total, _ = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    W = fq.CompressedWeight(torch.from_numpy((c.r.standard_normal((768, 512)) * 0.05).astype(np.float16)).cuda())
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 8, total, most, True), dtype=torch.uint8, device="cuda")
+    gws = torch.zeros(max(16, fq.flex_gemm_ws_bytes(total, 768, 512)), dtype=torch.uint8, device="cuda")
+    o = torch.empty((total, 512), dtype=torch.float16, device="cuda")
+    ys = [torch.empty((total, 768), dtype=torch.float16, device="cuda") for _ in range(12)]
+    fq.flex_dequant_gemm(want[:total].contiguous(), W, None, None, ys[0], total, fq.FLEX_EPI_NONE, gws)
+    first = ys[0].clone()
+    for i, y in enumerate(ys):
+        fq.flex_paged_attention(c.cache, qd, qd.stride(0), 8, kd, vd, kd.stride(0), o, None, cu, most, ws, total=total,
+                                accumulate=i % 2 == 1)
+        fq.flex_dequant_gemm(o, W, None, None, y, total, fq.FLEX_EPI_NONE, gws)
+    sync_status()
+    assert torch.equal(o, want[:total]) and all(torch.equal(y, first) for y in ys)
