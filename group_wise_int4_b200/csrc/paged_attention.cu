@@ -504,7 +504,6 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
 // 64: 72 us with the kernel below).
 template <bool LOOP>
 __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
-    pdl_trigger();
     const PagedView& c = A.c;
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
@@ -522,6 +521,7 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
     };
     int s0 = (blockIdx.x * 128 + threadIdx.x) * 4, row = find_row(s0);
     pdl_wait();                                               // the attention kernel writes what follows
+    pdl_trigger();
     if (LOOP ? s0 >= held : row < 0) return;
     const float2 stats = A.stats[static_cast<int64_t>(first) * A.plan.heads + head];
     for (;;) {
@@ -559,7 +559,6 @@ __global__ void __launch_bounds__(128, D == 64 ? 7 : 4) paged_weight_kernel(Attn
     constexpr int KB = D * BITS / 8, NG = D / GS, QR = 32, LD = D + 8;
     __shared__ __align__(16) __half sq[2][QR * LD];
     __shared__ float2 sl[2][QR];
-    pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
@@ -645,7 +644,10 @@ __global__ void __launch_bounds__(128, D == 64 ? 7 : 4) paged_weight_kernel(Attn
                 a[i / 2][2 * w + 1][2 + i % 2] = pr[w][3];
             }
         }
-        if (!waited) pdl_wait();
+        if (!waited) {
+            pdl_wait();
+            pdl_trigger();
+        }
         waited = true;
         load_stats(0);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};

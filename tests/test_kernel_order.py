@@ -44,3 +44,10 @@ def test_the_kernels_are_found():
 def test_tensor_memory_is_allocated_before_dependents_may_start(body):
     if "tmem_alloc(" in body:
         assert body.index("tmem_alloc(") < body.index("pdl_trigger(")
+
+
+@pytest.mark.parametrize("body", _kernels())
+def test_dependents_may_start_only_after_the_kernels_own_wait(body):
+    """The GEMM's early weight loads count on it: when its grid runs, all that came before the
+    kernel directly ahead of it is complete."""
+    assert body.index("pdl_wait(") < body.index("pdl_trigger(")
