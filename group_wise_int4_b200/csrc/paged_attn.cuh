@@ -282,9 +282,13 @@ __device__ __forceinline__ void put_stats(const AttnArgs& A, int64_t at, float t
     if (A.lse) A.lse[at] = sum == 0.f ? -INFINITY : fmaf(l, kLn2, top);
     if (A.stats) A.stats[at] = make_float2(top, sum == 0.f ? INFINITY : l);
 }
-// The probability of a score, by these statistics.
+// The probability of a score, by these statistics; 1 at most. A score that was summed again, in
+// another order, is off by roundings of its magnitude (by whole units above 2^23), which would make
+// "probabilities" of any size, infinity among them, and one of those would stay in the running
+// weights for good. NaN stays NaN.
 __device__ __forceinline__ float prob_of(float score, float2 stats) {
-    return exp2_fast(fmaf(score - stats.x, kLog2e, -stats.y));
+    const float x = fmaf(score - stats.x, kLog2e, -stats.y);
+    return exp2_fast(x > 0.f ? 0.f : x);
 }
 
 // Called by one warp of every unit and head: unit 0 says how many partial slots there are, a

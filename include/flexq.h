@@ -395,7 +395,9 @@ int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, void* v_out, 
  * accumulate != 0 (needs cache->weight): with p the attention probabilities,
  *   weight[slot] = (slot < ctx_len ? weight[slot] : 0) + sum of p over the sequence's new
  *   tokens and the heads that share the key head, for the slots [0, ctx_len + new tokens)
- *   (cross attention: [0, ctx_len)). Each slot's sum has a fixed order.
+ *   (cross attention: [0, ctx_len)). Each slot's sum has a fixed order. Scores may be summed
+ *   a second time for it, in another order than for o: each p is then off by a factor of
+ *   at most exp(2 (head_dim + 4) 2^-24 sum |q_i k_i|), and never above 1.
  * Infinities and NaN of a key or value reach the rows that attend to it, and no other row.
  * ws: flex_paged_attention_ws_bytes(...) bytes, nothing in it has to be set; calls that may
  * run at the same time need workspaces of their own. (With accumulate and one row a

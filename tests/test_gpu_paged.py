@@ -765,3 +765,22 @@ def test_a_gemm_right_behind_the_tiles(most):
         fq.flex_dequant_gemm(o, W, None, None, y, total, fq.FLEX_EPI_NONE, gws)
     sync_status()
     assert torch.equal(o, want[:total]) and all(torch.equal(y, first) for y in ys)
+
+
+@pytest.mark.parametrize("dim,bits", [(64, 4), (128, 4), (128, 8)])
+@pytest.mark.parametrize("share,n", [(1, [1, 1]), (4, [1, 1]), (1, [12, 3]), (2, [40, 5]), (1, [200, 40])])
+@pytest.mark.parametrize("size", [40.0, 3000.0, 20000.0])
+def test_weights_of_large_scores_are_probabilities(dim, bits, share, n, size):
+    """Scores of 1e4 to 1e10, whose fp32 sums are off by up to whole units: the pass that adds the
+    weights sums them in another order than the attention did, but what a row adds to a slot is
+    a probability all the same."""
+    c = Case(43, [150, 70], heads=2, dim=dim, bits=bits, room=max(n))
+    k, v = [(c.rows(m) * np.float16(size / 8)) for m in n], [c.rows(m) for m in n]
+    q = [c.rows(m, 2 * share) * np.float16(size / 4) for m in n]
+    c.cache.weight.zero_()
+    c.attend(q, k, v, accumulate=True, check=False)
+    for b, m in enumerate(n):
+        w = c.slots(c.cache.weight, b, int(c.ref.ctx[b]) + m).astype(np.float64)
+        assert np.isfinite(w).all()
+        assert w.min() >= 0 and w.max() <= m * share
+        assert (w.sum(1) > 0).all()
