@@ -567,6 +567,15 @@ def _need_rows(t, dtype, size, device, name, total, stride, width):
                          f"{t.untyped_storage().nbytes() // size - t.storage_offset()} elements are there")
 
 
+def _need_flat_rows(t, dtype, device, name, total, width):
+    """`total` rows of `width` elements, one after the other without a gap, are the tensor's own."""
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+    if not t.is_contiguous() or t.numel() < total * width:
+        raise ValueError(f"{name}: {total} contiguous rows of {width} elements expected, got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+
+
 def _rows_call(cache, cu, most, total, batch):
     """(batch, total, address of cu) of a ragged call, checked against cu's length."""
     if cu is None:
@@ -666,7 +675,7 @@ def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_n
     width, kv_width = n_heads * dim, cache.n_kv_heads * dim
     half = torch.float16
     _need_rows(q, half, 2, dev, "q", total, q_stride, width)
-    _need_rows(o, half, 2, dev, "o", total, width, width)
+    _need_flat_rows(o, half, dev, "o", total, width)
     if k_new is not None:
         _need_rows(k_new, half, 2, dev, "k_new", total, kv_stride, kv_width)
         k_new = k_new.data_ptr()
@@ -674,7 +683,7 @@ def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_n
         _need_rows(v_new, half, 2, dev, "v_new", total, kv_stride, kv_width)
         v_new = v_new.data_ptr()
     if lse is not None:
-        _need_rows(lse, torch.float32, 4, dev, "lse", total, n_heads, n_heads)
+        _need_flat_rows(lse, torch.float32, dev, "lse", total, n_heads)
         lse = lse.data_ptr()
     ws, size = _need_ws(ws, cache)
     _call(cache, stream, "flex_paged_attention", q.data_ptr(), q_stride, n_heads, k_new, v_new, kv_stride, o.data_ptr(), lse,

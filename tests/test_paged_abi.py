@@ -164,3 +164,23 @@ def test_binding_checks_rows():
         fq.flex_paged_attention(c, x, 128, 2, x, x, 128, x, torch.zeros((5, 2)), cu, 3, ws, total=6)
     with pytest.raises(ValueError, match="new_len"):
         fq.flex_paged_evict(c, 8, 4, torch.zeros(1, dtype=torch.int32), ws)
+
+
+def test_binding_refuses_outputs_with_a_stride_of_their_own():
+    """o and lse have no stride argument: a view of wider rows would be written across its neighbours."""
+    c = _py_cache(weight=True, slot_pos=True)
+    x, cu, ws = torch.zeros((6, 128), dtype=torch.float16), torch.zeros(3, dtype=torch.int32), torch.zeros(16, dtype=torch.uint8)
+    wide, wide_lse = torch.zeros((6, 160), dtype=torch.float16), torch.zeros((6, 4))
+
+    def call(o, lse):
+        fq.flex_paged_attention(c, x, 128, 2, x.clone(), x.clone(), 128, o, lse, cu, 3, ws, total=6)
+    for o in (wide[:, :128], wide[:, 32:], torch.zeros((9, 128), dtype=torch.float16)[3:8], torch.zeros((128, 6), dtype=torch.float16).T, torch.zeros((12, 128), dtype=torch.float16)[::2]):
+        with pytest.raises(ValueError, match="o: "):
+            call(o, None)
+    o = torch.zeros((7, 128), dtype=torch.float16)
+    for lse in (wide_lse[:, :2], torch.zeros((2, 6)).T):
+        with pytest.raises(ValueError, match="lse"):
+            call(o[:6], lse)
+    for good in (o, o[1:], o.view(-1), o.view(7, 2, 64)):                # any shape, as long as the rows follow each other
+        with pytest.raises(ValueError, match="CUDA"):                    # (the caches of this file have no device)
+            call(good, torch.zeros((6, 2)))
