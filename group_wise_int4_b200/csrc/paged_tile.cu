@@ -92,7 +92,10 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t base, int r, int c) {
 // maximum of 2^23 or more would leave factors that overflow: such rows' scores have m
 // subtracted in tensor memory first.
 __device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= 8388608.f && m != -FLT_MAX; }
-__device__ __forceinline__ float shift_of(float m) { return is_big(m) ? kLift : kLift - __fmul_rn(m, kLog2e); }
+// (No maximum yet: every score so far is -infinity, and its exponent is to stay that.)
+__device__ __forceinline__ float shift_of(float m) {
+    return m == -FLT_MAX || is_big(m) ? kLift : kLift - __fmul_rn(m, kLog2e);
+}
 __device__ __forceinline__ float lift_of(float m) {
     return m == -FLT_MAX || is_big(m) ? kLift : fmaf(m, kLog2e, shift_of(m));
 }
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(TileShape<D, TILES>::THREADS, TILES == 1 ? 2 :
         const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + TILES * 128 + tile * D + lanes;
         bool ok = tile < tiles;
         // the running maximum; the score from which it moves; what the fused exponent adds
-        float m = -FLT_MAX, limit = -FLT_MAX, shift = 0.f;
+        float m = -FLT_MAX, limit = -FLT_MAX, shift = kLift;
         uint64_t l = 0;                                          // two partial sums
         if (ok) {
             const uint4* qr = reinterpret_cast<const uint4*>(A.q + static_cast<int64_t>(u.first + token) * A.q_stride + h * D);

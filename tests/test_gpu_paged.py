@@ -784,3 +784,43 @@ def test_weights_of_large_scores_are_probabilities(dim, bits, share, n, size):
         assert np.isfinite(w).all()
         assert w.min() >= 0 and w.max() <= m * share
         assert (w.sum(1) > 0).all()
+
+
+@pytest.mark.parametrize("dim,bits", [(64, 4), (128, 8)])
+@pytest.mark.parametrize("n", [[1, 1], [3, 2], [12, 5], [40, 33], [150, 40]])
+def test_keys_of_minus_infinity_weigh_nothing(dim, bits, n):
+    """A fresh key whose score is -infinity adds nothing; a row with no other key gets zeros and a
+    log-sum-exp of -infinity, as one without any key."""
+    c = Case(45, [0, 20], heads=2, dim=dim, bits=bits, room=max(n))
+    q, k, v = [np.abs(x) for x in _scaled(c, n, 4)], [c.rows(m) for m in n], [c.rows(m) for m in n]
+    for x in q:
+        x[:] = np.maximum(x, np.float16(0.01))
+    k[0][0, :, 3] = -np.inf                                  # the first sequence's first key
+    k[1][-1, 1, 0] = -np.inf                                 # the other's last one, one key head
+    c.cache.weight.zero_()
+    o, ls = c.attend(q, k, v, accumulate=True, check=False)
+    got, ls = to_np(o).astype(np.float64), to_np(ls).astype(np.float64)
+    assert not got[0].any() and np.all(ls[0] == -np.inf)
+    assert np.isfinite(got).all() and np.isfinite(ls[1:]).all()
+    far = [x.copy() for x in k]
+    far[0][0, :, 3], far[1][-1, 1, 0] = 0, 0
+    for b, m in enumerate(n):
+        first = n[0] * b
+        for i in (range(1, m) if b == 0 else [m - 1]):
+            hide = 0 if b == 0 else m - 1
+            keep = [j for j in range(i + 1) if j != hide]
+            for h in (range(4) if b == 0 else (2, 3)):
+                g = h // 2
+                kk = np.concatenate([c.ref.values("k", b, g), far[b][keep, g].astype(np.float64)])
+                vv = np.concatenate([c.ref.values("v", b, g), v[b][keep, g].astype(np.float64)])
+                qi = q[b][i, h].astype(np.float64)
+                s = kk @ qi
+                p = np.exp(s - s.max())
+                want = p @ vv / p.sum()
+                size = (np.abs(kk) @ qi).max()
+                ep = 2 * (dim + 4) * E * size + 2.0 ** -21
+                tol = U * np.abs(want) + (U + 2 * ep + len(kk) * (E + 2.0 ** -25)) * np.abs(vv).max()
+                assert np.all(np.abs(got[first + i, h * dim:(h + 1) * dim] - want) <= tol), (b, i, h)
+                assert abs(ls[first + i, h] - s.max() - np.log(p.sum())) <= ep + len(kk) * E + 2 * E * abs(s.max())
+    w = c.slots(c.cache.weight, 0, n[0])
+    assert np.isfinite(w).all() and not w[:, 0].any()
