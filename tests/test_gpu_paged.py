@@ -786,6 +786,120 @@ def test_weights_of_large_scores_are_probabilities(dim, bits, share, n, size):
         assert (w.sum(1) > 0).all()
 
 
+def _exact_rows(c, n, factors, fine):
+    """Key rows of exact integers: 30 dims of the first half are 8 f 2^p (f: 0 or 1 a key), one of the
+    second half is the key's fine value, two more are 15 and 8. Each group spans 15 or 255
+    steps of a power of two, so the codes are exact."""
+    p, top = (12, 15) if c.bits == 4 else (8, 255)
+    x = np.zeros((n, c.heads, c.dim), np.float64)
+    x[:, :, :30] = 8 * np.asarray(factors)[:, None, None]
+    half = c.dim // 2
+    x[:, :, half] = np.asarray(fine)[:, None]
+    x[:, :, half + 1], x[:, :, half + 2] = 15, 8
+    x[:, :, c.group - 1::c.group] = top                      # and 0 is among the rest of every group
+    x[:, :, :half] *= 2.0 ** p
+    y = x.astype(np.float16)
+    assert np.array_equal(y, x)
+    return y
+
+
+# {of the 30 large dims, of the fine value, of 15, of 8}: scores of -2^30 to 2^30, below, across and
+# above 2^23, where the sums are exact and fine values differ by whole steps of fp32
+EXACT_QUERIES = [(8, 1, 34944, 15), (8, 1, 35968, 0), (0, 1, 0, 0), (4, 1, 0, 0), (-8, 1, 0, 0), (1024, 64, 0, 0), (16, 1, 0, 0),
+                 (0, 0.25, 2, 3), (32, 2, 0, 0), (-1024, 64, 0, 0), (-8, 1, -34944, -15), (8, 1, 34944, 14)]
+
+
+def _exact_queries(c, n, share, first=0):
+    x = np.zeros((n, c.heads * share, c.dim), np.float64)
+    half = c.dim // 2
+    for r in range(n * c.heads * share):
+        base, fine, a, b = EXACT_QUERIES[(r + r // 12 + first) % 12]
+        row = x.reshape(-1, c.dim)[r]
+        row[:30] = base * (1 if c.bits == 4 else 16)
+        row[half:half + 3] = fine, a, b
+    y = x.astype(np.float16)
+    assert np.array_equal(y, x)
+    return y
+
+
+def _check_exact(c, q, k, v, o, ls, before):
+    """The ordinary tolerances without the scores' own error, which is none here: an exponential's
+    argument is off by 4 e of the distance to the maximum (difference exact, factor and
+    product rounded), and the exponential by 2^-21."""
+    o, ls = to_np(o).astype(np.float64), to_np(ls).astype(np.float64)
+    at = 0
+    for b in range(len(q)):
+        n, nq = q[b].shape[:2]
+        share, ctx = nq // c.heads, int(c.ref.ctx[b])
+        ro, rl, sums, _ = c.ref.attend(b, q[b], None if k is None else k[b], None if v is None else v[b])
+        got = o[at:at + n].reshape(n, nq, c.dim)
+        keys = sums.shape[1]
+        ep = np.zeros((n, nq))
+        for g in range(c.heads):
+            kk = c.ref.values("k", b, g)
+            if k is not None:
+                kk = np.concatenate([kk, k[b][:, g].astype(np.float64)])
+            for h in range(g * share, (g + 1) * share):
+                for i in range(n):
+                    s = kk[:ctx + (0 if k is None else i + 1)] @ q[b][i, h].astype(np.float64)
+                    assert np.array_equal(s, s.astype(np.float32))
+                    far = s.max(initial=-np.inf) - s
+                    ep[i, h] = 8 * E * far[far < 100].max(initial=0) + 2.0 ** -21      # beyond: below every bound
+        vmax = max([np.abs(c.ref.values("v", b, g)).max(initial=0) for g in range(c.heads)] +
+                   ([] if v is None else [np.abs(v[b].astype(np.float64)).max(initial=0)]))
+        tol = U * np.abs(ro) + (U + 2 * ep + keys * (E + 2.0 ** -25))[..., None] * vmax
+        assert np.all(np.abs(got - ro) <= tol), (b, (np.abs(got - ro) - tol).max())
+        some = np.isfinite(rl)
+        assert np.array_equal(np.isfinite(ls[at:at + n]), some)
+        bound = ep + keys * E + 2 * E * np.abs(np.where(some, rl, 0))
+        assert np.all(np.abs(np.where(some, ls[at:at + n] - rl, 0)) <= bound), b
+        if before is not None:
+            grown = ctx + (0 if k is None else n)
+            old, new = (c.slots(t, b, grown).astype(np.float64) for t in (before, c.cache.weight))
+            old[:, ctx:] = 0
+            bound = (2 * ep.max() + (keys + n * share + 4) * E) * sums + 2 * E * np.abs(old + sums) + 1e-30
+            assert np.all(np.abs(new - old - sums) <= bound), (b, np.abs(new - old - sums).max())
+        at += n
+
+
+@pytest.mark.parametrize("dim,bits,group", [(64, 4, 32), (128, 4, 64), (64, 8, 32), (128, 8, 64)])
+@pytest.mark.parametrize("share,n", [(1, [1, 1]), (4, [1, 1]), (1, [6, 2]), (2, [6, 1]), (1, [24, 3]), (1, [40, 30]), (3, [20, 9]),
+                                     (1, [140, 70])])
+@pytest.mark.parametrize("cross", [False, True])
+def test_scores_around_two_to_the_23rd(dim, bits, group, share, n, cross):
+    """Rows whose scores are below, across and above 2^23, up to 2^30 and of both signs, side by side
+    in one tile, and in one row keys of which some score near 0: the maximum moves between
+    the ranges, and every difference of a few units counts in full."""
+    ctx = [300, 90]
+    c = Case(44, ctx, heads=2, dim=dim, bits=bits, group=group, page=16, room=max(n))
+    r = c.r
+
+    def keys(m, start):
+        at = np.arange(start, start + m)
+        # 64 keys near 0, 64 far, then in runs of 5; fine values that rise, fall and scatter
+        far = np.where(at < 128, at >= 64, at // 5 % 3 > 0)
+        return _exact_rows(c, m, far, np.where(at % 7 < 3, at // 24 % 16, r.integers(0, 16, m)))
+    for b, m in enumerate(ctx):
+        ids = range(m)
+        x = keys(m, 0)
+        c.ref.ctx[b] = 0
+        c.ref.store(b, x, c.rows(m))
+        c.ref.ctx[b] = m
+        for j in ids:
+            p, s = c.ref.at(b, j)
+            for name in "kv":
+                getattr(c.cache, name + "_codes")[p, :, s] = torch.from_numpy(c.ref.codes[name][p, :, s]).cuda()
+                getattr(c.cache, name + "_meta")[p, :, s] = torch.from_numpy(c.ref.meta[name][p, :, s]).cuda()
+        assert all(np.array_equal(c.ref.values("k", b, g), x[:, g].astype(np.float64)) for g in range(2))
+    q = [_exact_queries(c, m, share, first=i) for i, m in enumerate(n)]
+    k, v = (None, None) if cross else ([keys(m, 40 + 9 * i) for i, m in enumerate(n)], [c.rows(m) for m in n])
+    for acc in (False, True):
+        c.cache.weight.zero_()
+        before = c.cache.weight.clone() if acc else None
+        o, ls = c.attend(q, k, v, accumulate=acc, check=False)
+        _check_exact(c, q, k, v, o, ls, before)
+
+
 @pytest.mark.parametrize("dim,bits", [(64, 4), (128, 8)])
 @pytest.mark.parametrize("n", [[1, 1], [3, 2], [12, 5], [40, 33], [150, 40]])
 def test_keys_of_minus_infinity_weigh_nothing(dim, bits, n):
