@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
     };
 
     // ---- fresh keys, by the last part
+    bool wild = false;                                      // one of their values is infinite or NaN
     if (A.k_new != nullptr && u.part == u.parts - 1) {
         const int last = (min(row_end, row0 + R) - 1) / share + 1;          // keys any row sees
         const int64_t kv_stride = A.kv_stride;
@@ -282,36 +283,18 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
                                        : make_uint4(0, 0, 0, 0);
             }
             // A hidden key's probability is 0, and 0 * infinity would be NaN: infinities and
-            // NaN leave the product and are added for the rows that see them.
-            bool wild = false;
+            // NaN leave the product and are added, at the end, for the rows that see them.
+            bool here = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int w = 0; w < D / 64; ++w) wild |= any_wild(x[k][w]);
-            if (__any_sync(0xffffffffu, wild)) {
+                for (int w = 0; w < D / 64; ++w) here |= any_wild(x[k][w]);
+            if (__any_sync(0xffffffffu, here)) {
+                wild = true;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int w = 0; w < D / 64; ++w) x[k][w] = without_wild(x[k][w]);
-                for (int k = 0; k < 16 && j0 + k < last; ++k) {
-                    const __half* vr = vf + static_cast<int64_t>(j0 + k) * kv_stride + g * (D / 8);
-#pragma unroll
-                    for (int n = 0; n < NR; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // pb's lane (row, key / 2) holds keys 2t, 2t + 1 and their next 8
-                            const uint32_t w = __shfl_sync(0xffffffffu, k < 8 ? pb[0][n][0] : pb[0][n][1],
-                                                           (2 * t + e) * 4 + ((k & 7) >> 1));
-                            const float pr = (k & 1) ? h2f_hi(w) : h2f_lo(w);
-                            if (j0 + k > token[n][e] || (TWICE && t >= 2)) continue;
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                const float v0 = __half2float(vr[2 * i]), v1 = __half2float(vr[2 * i + 1]);
-                                if (!isfinite(v0)) acc[i][n][e] = fmaf(pr, v0, acc[i][n][e]);
-                                if (!isfinite(v1)) acc[i][n][2 + e] = fmaf(pr, v1, acc[i][n][2 + e]);
-                            }
-                        }
-                }
             }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -472,6 +455,18 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
             for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             const int r = n * 8 + 2 * t + e;
             if (row0 + r >= row_end) continue;
+            // whatever their weight, which is positive, the sum is what they make it
+            if (wild) {
+                for (int j = 0; j <= token[n][e]; ++j) {
+                    const __half* vr = A.v_new + static_cast<int64_t>(u.first + j) * A.kv_stride + head * D + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const float v0 = __half2float(vr[2 * i]), v1 = __half2float(vr[2 * i + 1]);
+                        if (!isfinite(v0)) acc[i][n][e] += v0;
+                        if (!isfinite(v1)) acc[i][n][2 + e] += v1;
+                    }
+                }
+            }
             if (u.parts == 1) {
                 const int64_t at = static_cast<int64_t>(u.first + token[n][e]) * (A.plan.heads * share) + head * share + row0 + r - token[n][e] * share;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;

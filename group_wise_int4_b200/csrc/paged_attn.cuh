@@ -347,8 +347,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs A) {
             const float* p = A.parts + ((static_cast<int64_t>(slot - rec.part) * plan.heads + head) * R + r) * (D + 4);
             float top = -FLT_MAX, sum = 0.f;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            // (not 0: an infinite value of a part with a far smaller maximum stays what it is, and what is
+            // finite of it is below every last place; NaN stays NaN)
+            auto factor = [](float m, float t) {
+                const float f = exp2_fast(exponent_of(m, t));
+                return f < FLT_MIN ? FLT_MIN : f;
+            };
             auto add = [&](float2 ml, float4 x) {
-                const float t = fmaxf(top, ml.x), f0 = exp2_fast(exponent_of(top, t)), f = exp2_fast(exponent_of(ml.x, t));
+                const float t = fmaxf(top, ml.x), f0 = factor(top, t), f = factor(ml.x, t);
                 top = t;
                 sum = fmaf(sum, f0, f * ml.y);
                 a.x = fmaf(a.x, f0, f * x.x);

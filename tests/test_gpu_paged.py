@@ -938,3 +938,52 @@ def test_keys_of_minus_infinity_weigh_nothing(dim, bits, n):
                 assert abs(ls[first + i, h] - s.max() - np.log(p.sum())) <= ep + len(kk) * E + 2 * E * abs(s.max())
     w = c.slots(c.cache.weight, 0, n[0])
     assert np.isfinite(w).all() and not w[:, 0].any()
+
+
+@pytest.mark.parametrize("dim,bits", [(64, 4), (128, 4), (64, 8), (128, 8)])
+@pytest.mark.parametrize("ctx,n", [([30, 0], [1, 2]), ([30, 0], [4, 3]), ([30, 0], [12, 9]), ([30, 0], [40, 20]), ([30, 0], [150, 40]),
+                                   ([5000, 700], [1, 2]), ([5000, 700], [12, 3]), ([5000, 700], [60, 3]), ([9000, 700], [150, 3])])
+def test_infinite_values_of_any_weight(dim, bits, ctx, n):
+    """An infinite fresh value makes its dim infinite in every row that sees it, however small its
+    weight (it underflows fp16 and, where the parts of a long history are joined, fp32), in every
+    kernel alike; the other dims have the bits that a value of 0 gives."""
+    c = Case(46, ctx, heads=1, dim=dim, bits=bits, page=64, room=max(n))
+    q, k, v = [np.abs(x) for x in _scaled(c, n, 2)], [c.rows(m) for m in n], [c.rows(m) for m in n]
+    at = [n[0] // 2, 0]
+    zero = [x.copy() for x in v]
+    for b, j in enumerate(at):
+        k[b][j] = -300 if ctx[b] < 1000 else -3000           # about 50 dims' worth below the other scores
+        q[b][:] = np.maximum(q[b], np.float16(0.05))
+        v[b][j, 0, 5], v[b][j, 0, dim - 1] = np.inf, -np.inf
+        zero[b][j, 0, 5] = zero[b][j, 0, dim - 1] = 0
+    want, wl = c.attend(q, k, zero)
+    o, ls = c.attend(q, k, v, check=False)
+    assert torch.equal(ls, wl)
+    got, want = (to_np(x).reshape(-1, 2, dim) for x in (o, want))
+    seen = np.zeros(len(got), bool)
+    seen[at[0]:n[0]] = seen[n[0] + at[1]:n[0] + n[1]] = True
+    rest = [d for d in range(dim) if d not in (5, dim - 1)]
+    assert np.array_equal(got[..., rest].view(np.uint16), want[..., rest].view(np.uint16))
+    assert np.array_equal(got[~seen].view(np.uint16), want[~seen].view(np.uint16))
+    if ctx[1] == 0:                                          # its first row sees nothing else
+        seen[n[0]] = False
+    assert np.all(got[seen][..., 5] == np.inf) and np.all(got[seen][..., dim - 1] == -np.inf)
+
+
+@pytest.mark.parametrize("n", [1, 3, 12, 60, 150])
+def test_infinite_values_in_a_part_of_no_weight(n):
+    """The last part of a long history, the fresh keys' own, has scores some hundreds below the first
+    part's: joined, its factor underflows."""
+    c = Case(47, [0], heads=1, dim=64, page=64, room=6000 + n)
+    low = np.abs(c.rows(6000)) + np.float16(1)
+    low[3000:] *= -20
+    low[:3000] *= 20
+    c.store([low], [c.rows(6000)], advance=True)
+    q, k, v = [np.abs(_scaled(c, [n], 1)[0]) + np.float16(0.1)], [-20 * (np.abs(c.rows(n)) + np.float16(1))], [c.rows(n)]
+    want, wl = c.attend(q, k, v)
+    v[0][0, 0, 5], v[0][0, 0, 40] = np.inf, np.nan
+    o, ls = c.attend(q, k, v, check=False)
+    assert torch.equal(ls, wl)
+    rest = [d for d in range(64) if d not in (5, 40)]
+    assert torch.equal(o[:n, rest], want[:n, rest])
+    assert bool((o[:n, 5] == float("inf")).all()) and bool(o[:n, 40].isnan().all())
