@@ -56,11 +56,15 @@ __device__ __forceinline__ int rows_of(const RowsOf& r, int b, int& first, int* 
 
 __device__ __forceinline__ int paged_capacity(const PagedView& c) { return c.max_pages << c.shift; }
 
-// Slots that sequence b holds, within the table.
+// Slots that sequence b holds; -1, reported, where ctx_len is no length of the table: nothing of
+// such a sequence is read or written, since what it holds is not known.
 __device__ __forceinline__ int slots_of(const PagedView& c, int b) {
-    const int n = __ldg(c.ctx_len + b), cap = paged_capacity(c);
-    if (n < 0 || n > cap) paged_bad(c);
-    return min(max(n, 0), cap);
+    const int n = __ldg(c.ctx_len + b);
+    if (static_cast<unsigned>(n) > static_cast<unsigned>(paged_capacity(c))) {
+        paged_bad(c);
+        return -1;
+    }
+    return n;
 }
 
 // Page of slot s of sequence b (s within the table); -1, reported, where the id is not a

@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
     const int n = rows_of(A.rows, b, first, c.status);
-    const int ctx = slots_of(c, b), held = n > 0 ? ctx + (A.k_new != nullptr) : 0, cap = paged_capacity(c);
+    const int ctx = slots_of(c, b), held = n > 0 && ctx >= 0 ? ctx + (A.k_new != nullptr) : 0, cap = paged_capacity(c);
     // four slots of one page at a time; their row, -1: none
     auto find_row = [&](int s0) {
         if (s0 >= held) return -1;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(128, D == 64 ? 7 : 4) paged_weight_kernel(Attn
     const int head = blockIdx.y, b = blockIdx.z;
     int first;
     const int n = rows_of(A.rows, b, first, c.status), ctx = slots_of(c, b), cap = paged_capacity(c);
-    const int old_blocks = (ctx + 127) / 128, blocks = n == 0 ? 0 : old_blocks + (k_new ? (n + 127) / 128 : 0);
+    const int old_blocks = (ctx + 127) / 128, blocks = n == 0 || ctx < 0 ? 0 : old_blocks + (k_new ? (n + 127) / 128 : 0);
     bool waited = false;
     for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
         const bool fresh = block >= old_blocks;

@@ -161,6 +161,7 @@ __device__ __forceinline__ Unit find_unit(const PagedView& c, const RowsOf& rows
         if (b < p.batch) {
             s.n = rows_of(rows, b, s.first, c.status);
             s.ctx = slots_of(c, b);
+            if (s.ctx < 0) s.n = s.ctx = 0;             // no rows
             s.tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.share + R - 1) / R);
         }
         return s;
@@ -303,7 +304,7 @@ __device__ __forceinline__ void record_split(const AttnArgs& A, const Unit& u, i
             int first;
             const int n = rows_of(A.rows, b, first, A.c.status);
             const int64_t tiles = (static_cast<int64_t>(n) * A.plan.share + R - 1) / R;
-            const int parts = ((slots_of(A.c, b) + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per;
+            const int parts = ((max(slots_of(A.c, b), 0) + KEYS - 1) / KEYS + u.plan_per - 1) / u.plan_per;
             if (parts > 1) units += tiles * parts;
         }
 #pragma unroll

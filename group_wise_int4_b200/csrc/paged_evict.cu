@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(PS_T, U == 1 ? 7 : 4) evict_small_kernel(Paged
     pdl_trigger();
     const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = slots_of(c, b);
-    if (head == 0 && tid == 0) new_len[b] = min(n, budget);
+    if (head == 0 && tid == 0) new_len[b] = n < 0 ? __ldg(c.ctx_len + b) : min(n, budget);      // (a wrong length stays one)
     if (n <= budget) return;
     for (int i = tid; i < (n + (1 << c.shift) - 1) >> c.shift; i += PS_T) pages[i] = page_of(c, b, i << c.shift);
     __syncthreads();
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(PE_THREADS) evict_select_kernel(PagedView c, i
     const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     int32_t* list = moves_of(ws, b * c.heads + head, most);
     const int n = slots_of(c, b);
-    if (head == 0 && tid == 0) new_len[b] = min(n, budget);
+    if (head == 0 && tid == 0) new_len[b] = n < 0 ? __ldg(c.ctx_len + b) : min(n, budget);
     if (n <= budget) {
         if (tid == 0) list[0] = 0;
         return;

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(PS_THREADS) paged_store_kernel(PagedView c, Ro
         }
     }
     const int ctx = slots_of(c, b);
+    if (ctx < 0) return;
     const int start = pos0 ? __ldg(pos0 + b) : ctx;
     const SlotRows<TOKENS> slots(c, b, static_cast<int64_t>(ctx) + t0, count);
     uint8_t* const codes = (which ? c.vc : c.kc) + d * BITS / 8;

@@ -356,7 +356,9 @@ int flex_layernorm(const void* x, const void* g, const void* b, void* y, int64_t
  * What only the device can see - a page id outside [0, num_pages), ctx_len outside
  * [0, max_pages*page_size], cu that decreases or exceeds most or total, a new slot behind
  * the table - is reported as FLEX_ERR_INVALID_ARG by flex_get_status; the sequence or
- * slot concerned is skipped or its results are unspecified, all others are right.        */
+ * slot concerned is skipped or its results are unspecified, all others are right (where cu
+ * gives the same rows to several sequences, all results are unspecified). A sequence with a
+ * wrong ctx_len keeps its slots, positions and weights as they were.                      */
 typedef struct {
     void *k_codes, *k_meta, *v_codes, *v_meta;
     float* weight;
@@ -420,7 +422,7 @@ int flex_paged_attention(const flex_paged_cache* cache, const void* q, int64_t q
  * counts as -infinity. The i-th slot below the budget that is given up takes codes,
  * metadata, weight and position of the i-th kept slot behind it; nothing else moves, and
  * slots from the budget on keep their old contents. new_len[b] = min(ctx_len[b], budget)
- * (device int32 [batch], not overlapping ctx_len). 0 <= recent <= budget, budget > 0.
+ * (device int32 [batch], not overlapping ctx_len; a wrong ctx_len as it is). 0 <= recent <= budget, budget > 0.
  * Needs weight and slot_pos. A page must belong to one sequence only, and once. Heads hold
  * different tokens afterwards, in no order: attention over the cache needs none.
  * ws: flex_paged_evict_ws_bytes(cache, budget) bytes, as for the attention. */

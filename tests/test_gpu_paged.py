@@ -987,3 +987,38 @@ def test_infinite_values_in_a_part_of_no_weight(n):
     rest = [d for d in range(64) if d not in (5, 40)]
     assert torch.equal(o[:n, rest], want[:n, rest])
     assert bool((o[:n, 5] == float("inf")).all()) and bool(o[:n, 40].isnan().all())
+
+
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), 1 << 20, (1 << 31) - 1, "one too many"])
+@pytest.mark.parametrize("n", [[1, 1, 1], [3, 40, 2]])
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_sequence_of_impossible_length_keeps_its_cache(bad, n, wide):
+    """A ctx_len outside the table is reported and nothing of its sequence changes: no slot, position
+    or weight, in the store, the running weights and the eviction (of both kinds of table);
+    its new length stays what it was, so that it is reported again. The others are right."""
+    c = Case(48, [40, 90, 25], heads=2, dim=64, page=64, room=2300 if wide else 45)
+    cap = c.cache.page_table.shape[1] * c.page
+    c.cache.weight.copy_(torch.from_numpy(np.abs(c.r.standard_normal(tuple(c.cache.weight.shape))).astype(np.float32)))
+    c.ref.weight = to_np(c.cache.weight).astype(np.float64)
+    q, k, v = _scaled(c, n, 4), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    o = torch.empty((total, 4 * c.dim), dtype=torch.float16, device="cuda")
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 4, total, most, True), dtype=torch.uint8, device="cuda")
+    pools = lambda: [getattr(c.cache, x) for x in ("k_codes", "k_meta", "v_codes", "v_meta", "weight", "slot_pos")]
+    mine = torch.as_tensor([x for x in to_np(c.cache.page_table[1]) if x >= 0], dtype=torch.int64, device="cuda")
+    before = [x[mine].clone() for x in pools()]
+
+    def same():
+        return all(torch.equal(x[mine].view(torch.uint8), y.view(torch.uint8)) for x, y in zip(pools(), before))
+    value = cap + 1 if bad == "one too many" else bad
+    c.ctx[1] = value
+    fq.flex_paged_attention(c.cache, qd, qd.stride(0), 4, kd, vd, kd.stride(0), o, None, cu, most, ws, total=total, accumulate=True)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG and same()
+    fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), cu, most, total=total)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG and same()
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(c.cache, 20), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(c.cache, 20, 5, new, ew)
+    assert _status() == fq.FLEX_ERR_INVALID_ARG and same()
+    assert new.tolist() == [20, value, 20]
