@@ -576,11 +576,18 @@ def _need_flat_rows(t, dtype, device, name, total, width):
                          f"strides {t.stride()}")
 
 
+def _too_large(**sizes):
+    raise ValueError("a size does not fit 32 bits: " + ", ".join(f"{k} = {v}" for k, v in sizes.items()))
+
+
 def _rows_call(cache, cu, most, total, batch):
     """(batch, total, address of cu) of a ragged call, checked against cu's length."""
     if cu is None:
         batch = cache.batch if batch is None else int(batch)
-        return batch, batch * int(most), None
+        total = batch * int(most)
+        if (most | total | batch) >> 31 > 0:
+            _too_large(most=most, batch=batch)
+        return batch, total, None
     if cu.dtype is not torch.int32 or cu.device != cache.device or cu.dim() != 1 or not cu.is_contiguous():
         _need(cu, torch.int32, cache.device, "cu", (None,))
     n = cu.numel()
@@ -590,6 +597,8 @@ def _rows_call(cache, cu, most, total, batch):
         raise ValueError(f"cu: {batch + 1} offsets expected, got {n}")
     if total is None:
         raise ValueError("total: the number of rows that cu may reach is needed with cu")
+    if (most | total | batch) >> 31 > 0:
+        _too_large(most=most, total=total, batch=batch)
     return batch, total, cu.data_ptr()
 
 
@@ -660,6 +669,8 @@ def _size(n, what):
 
 
 def flex_paged_attention_ws_bytes(cache: FlexPagedCache, n_heads, total, most, accumulate=False, batch=None) -> int:
+    if (n_heads | total | most) >> 31 > 0 or (batch or 0) >> 31 > 0:
+        _too_large(n_heads=n_heads, total=total, most=most, batch=batch)
     with torch.cuda.device(cache.device):
         n = lib().flex_paged_attention_ws_bytes(cache.ref(), n_heads, cache.batch if batch is None else batch, total,
                                                 most, 1 if accumulate else 0)
@@ -671,6 +682,8 @@ def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_n
     """Attention of new tokens over the cached slots and their own fresh keys/values (k_new and
     v_new None: cross attention, over the slots alone). lse: fp32 [total][n_heads] or None."""
     batch, total, cu = _rows_call(cache, cu_new, most, total, batch)
+    if n_heads >> 31 > 0:
+        _too_large(n_heads=n_heads)
     dev, dim = cache.device, cache.head_dim
     width, kv_width = n_heads * dim, cache.n_kv_heads * dim
     half = torch.float16
@@ -691,6 +704,8 @@ def flex_paged_attention(cache: FlexPagedCache, q, q_stride, n_heads, k_new, v_n
 
 
 def flex_paged_evict_ws_bytes(cache: FlexPagedCache, budget) -> int:
+    if budget >> 31 > 0:
+        _too_large(budget=budget)
     return _size(lib().flex_paged_evict_ws_bytes(cache.ref(), budget), "flex_paged_evict_ws_bytes")
 
 
@@ -698,6 +713,8 @@ def flex_paged_evict(cache: FlexPagedCache, budget, recent, new_len, ws, stream=
     """Keep `budget` slots of every longer sequence and key head: the `recent` latest positions, then
     the largest weights. new_len (int32 [batch]) takes min(ctx_len, budget)."""
     _need(new_len, torch.int32, cache.device, "new_len", (cache.batch,))
+    if (budget | recent) >> 31 > 0:
+        _too_large(budget=budget, recent=recent)
     ws, size = _need_ws(ws, cache)
     _call(cache, stream, "flex_paged_evict", budget, recent, new_len.data_ptr(), ws, size)
 

@@ -184,3 +184,33 @@ def test_binding_refuses_outputs_with_a_stride_of_their_own():
     for good in (o, o[1:], o.view(-1), o.view(7, 2, 64)):                # any shape, as long as the rows follow each other
         with pytest.raises(ValueError, match="CUDA"):                    # (the caches of this file have no device)
             call(good, torch.zeros((6, 2)))
+
+
+def test_binding_refuses_sizes_that_do_not_fit_the_call():
+    """The C arguments are 32 bits wide and ctypes cuts what does not fit: a budget of 2^32 + 5 slots
+    would keep 5."""
+    c = _py_cache(weight=True, slot_pos=True)
+    x, cu, ws = torch.zeros((6, 128), dtype=torch.float16), torch.zeros(3, dtype=torch.int32), torch.zeros(1 << 20, dtype=torch.uint8)
+    new = torch.zeros(2, dtype=torch.int32)
+    big = (1 << 32) + 5
+    for budget, recent in ((big, 4), (1 << 31, 4), (8, 1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fq.flex_paged_evict(c, budget, recent, new, ws)
+        if recent == 4:
+            with pytest.raises(ValueError, match="32 bits"):
+                fq.flex_paged_evict_ws_bytes(c, budget)
+    for call in (lambda **kw: fq.flex_paged_store_kv(c, x, x, 128, cu, **kw), lambda **kw: fq.flex_paged_load_kv(c, x, x, 128, cu, **kw),
+                 lambda **kw: fq.flex_paged_attention(c, x, 128, 2, x, x, 128, x.clone(), None, cu, ws=ws, **kw)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(most=big, total=6)
+        with pytest.raises(ValueError, match="32 bits"):
+            call(most=3, total=big)
+        with pytest.raises(ValueError, match="32 bits|offsets"):
+            call(most=3, total=6, batch=big)
+    with pytest.raises(ValueError, match="32 bits"):
+        fq.flex_paged_store_kv(c, x, x, 128, None, big)
+    for kw in (dict(n_heads=big, total=6, most=3), dict(n_heads=2, total=big, most=3), dict(n_heads=2, total=6, most=big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fq.flex_paged_attention_ws_bytes(c, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        fq.flex_paged_attention(c, x, 128, big, x, x, 128, x.clone(), None, cu, 3, ws, total=6)
