@@ -486,8 +486,8 @@ class FlexPagedCache:
     (k_codes, k_meta, v_codes, v_meta): codes uint8 [num_pages][n_kv_heads][page_size]
     [head_dim*bits/8], meta fp16 [num_pages][n_kv_heads][page_size][head_dim/group][2].
     weight: True, or an fp32 tensor [num_pages][n_kv_heads][page_size], to accumulate
-    attention weights; slot_pos: the same with int32, to keep positions. Eviction needs
-    both."""
+    attention weights (None or False: none); slot_pos: the same with int32, to keep
+    positions. Eviction needs both."""
 
     def __init__(self, page_table, ctx_len, num_pages=None, page_size=None, n_kv_heads=None, head_dim=None,
                  num_bits=4, group_size=64, pools=None, weight=None, slot_pos=None):
@@ -508,6 +508,7 @@ class FlexPagedCache:
             weight = torch.zeros(shape, dtype=torch.float32, device=dev)
         if slot_pos is True:
             slot_pos = torch.zeros(shape, dtype=torch.int32, device=dev)
+        weight, slot_pos = (None if x is False else x for x in (weight, slot_pos))
         self.page_table, self.ctx_len, self.weight, self.slot_pos = page_table, ctx_len, weight, slot_pos
         self.batch, self.max_pages = page_table.shape
         self.struct()
@@ -549,6 +550,8 @@ class FlexPagedCache:
 
 def _need(t, dtype, device, name, shape=None):
     """A contiguous tensor of this dtype, device and shape (None: any extent)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor expected, got {t!r}")
     if t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
     if not t.is_contiguous() or (shape is not None and (t.dim() != len(shape) or any(

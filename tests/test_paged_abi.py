@@ -214,3 +214,12 @@ def test_binding_refuses_sizes_that_do_not_fit_the_call():
             fq.flex_paged_attention_ws_bytes(c, **kw)
     with pytest.raises(ValueError, match="32 bits"):
         fq.flex_paged_attention(c, x, 128, big, x, x, 128, x.clone(), None, cu, 3, ws, total=6)
+
+
+def test_a_cache_without_weights_may_say_so():
+    c = _py_cache(weight=False, slot_pos=False)
+    assert c.weight is None and c.slot_pos is None and not c.struct().weight and not c.struct().slot_pos
+    with pytest.raises(ValueError, match="weight"):
+        _py_cache(weight=1)
+    with pytest.raises(ValueError, match="slot_pos"):
+        _py_cache(slot_pos=1)
