@@ -1022,3 +1022,40 @@ def test_a_sequence_of_impossible_length_keeps_its_cache(bad, n, wide):
     fq.flex_paged_evict(c.cache, 20, 5, new, ew)
     assert _status() == fq.FLEX_ERR_INVALID_ARG and same()
     assert new.tolist() == [20, value, 20]
+
+
+@pytest.mark.parametrize("bits,group", [(4, 32), (8, 64)])
+@pytest.mark.parametrize("n", [1, 5, 9, 40])
+def test_steps_of_every_scale(bits, group, n):
+    """The step that attention takes for a scale is the correctly rounded fp16(1 / scale), for every
+    positive fp16 scale whose reciprocal is finite there: one slot a head, code 1, minimum 0, so
+    that the output is the step itself; 1, 5 and 9 rows of the rows kernel, 40 of the tiles."""
+    scales = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16)
+    with np.errstate(over="ignore"):
+        want = (1.0 / scales.astype(np.float64)).astype(np.float16)
+    scales, want = scales[np.isfinite(want)], want[np.isfinite(want)]
+    assert scales[0] < 1.6e-5 and scales[-1] == 65504 and len(scales) > 30000
+    heads, dim = 64, 64
+    pages = -(-len(scales) // heads)
+    table, ctx = torch.arange(pages, dtype=torch.int32, device="cuda").view(-1, 1), torch.ones(pages, dtype=torch.int32, device="cuda")
+    cache = fq.FlexPagedCache(table, ctx, pages, 16, heads, dim, bits, group)
+    padded = np.resize(scales, (pages, heads))
+    for codes, meta in ((cache.k_codes, cache.k_meta), (cache.v_codes, cache.v_meta)):
+        codes.fill_(0x11 if bits == 4 else 1)
+        meta[:, :, 0, :, 1] = torch.from_numpy(padded).cuda()[:, :, None]
+    # keys: the same values; a query of zeros, so that only the value's step is in the output
+    total = pages * n
+    q = torch.zeros((total, heads * dim), dtype=torch.float16, device="cuda")
+    o = torch.empty_like(q)
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(cache, heads, total, n), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_attention(cache, q, heads * dim, heads, None, None, 0, o, None, None, n, ws)
+    sync_status()
+    got = to_np(o).reshape(pages, n, heads, dim).transpose(0, 2, 1, 3).reshape(pages * heads, n, dim)[:len(scales)]
+    assert np.array_equal(got.view(np.uint16), np.broadcast_to(want[:, None, None], got.shape).view(np.uint16))
+    # and the keys': a query of one 1 in a dim, against the log-sum-exp of the one score
+    q.view(total, heads, dim)[:, :, 17] = 1
+    ls = torch.empty((total, heads), device="cuda")
+    fq.flex_paged_attention(cache, q, heads * dim, heads, None, None, 0, o, ls, None, n, ws)
+    sync_status()
+    got = to_np(ls).reshape(pages, n, heads).transpose(0, 2, 1).reshape(pages * heads, n)[:len(scales)]
+    assert np.all(np.abs(got - want.astype(np.float64)[:, None]) <= 2 * E * want.astype(np.float64)[:, None] + 2.0 ** -21)
