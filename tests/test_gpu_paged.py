@@ -1059,3 +1059,114 @@ def test_steps_of_every_scale(bits, group, n):
     sync_status()
     got = to_np(ls).reshape(pages, n, heads).transpose(0, 2, 1).reshape(pages * heads, n)[:len(scales)]
     assert np.all(np.abs(got - want.astype(np.float64)[:, None]) <= 2 * E * want.astype(np.float64)[:, None] + 2.0 ** -21)
+
+
+@pytest.mark.parametrize("per", [2, 20])
+def test_moves_and_weights_behind_32_bit_offsets(per):
+    """The last pages of a pool of 5.4 GB: accumulated weights, and what eviction moves (codes,
+    metadata, weights, positions) in tables of up to 2048 slots and of more."""
+    pages, heads, page, dim = 1 << 13, 40, 128, 128
+    ids = pages - 1 - np.random.default_rng(23).permutation(per)
+    table = torch.from_numpy(ids.astype(np.int32)).cuda().view(1, per)
+    held = per * page - 9
+    ctx = torch.tensor([held], dtype=torch.int32, device="cuda")
+    shape = (pages, heads, page)
+    pools = tuple(torch.empty(shape + s, dtype=t, device="cuda") for s, t in
+                  (((dim,), torch.uint8), ((2, 2), torch.float16)) * 2)
+    cache = fq.FlexPagedCache(table, ctx, pools=pools, weight=True, slot_pos=True, num_bits=8, group_size=64)
+    r = np.random.default_rng(24)
+    ref = PagedCache([np.arange(per)], [held], per, page, 1, dim, 8, 64)
+    used = torch.from_numpy(ids.copy()).cuda()
+    for codes, meta in ((pools[0], pools[1]), (pools[2], pools[3])):
+        codes[used] = torch.from_numpy(r.integers(0, 256, (per, heads, page, dim), dtype=np.uint8)).cuda()
+        m = np.stack([r.standard_normal((per, heads, page, 2)) - 1, 60 + 50 * r.random((per, heads, page, 2))], -1)
+        meta[used] = torch.from_numpy(m.astype(np.float16)).cuda()
+    cache.weight[used] = torch.from_numpy(r.random((per, heads, page), dtype=np.float32)).cuda()
+    pos = r.permutation(per * page * heads).astype(np.int32).reshape(per, heads, page)
+    cache.slot_pos[used] = torch.from_numpy(pos).cuda()
+    for n in (1, 3, 33):
+        q = (r.standard_normal((n, heads, dim)) * 0.09).astype(np.float16)
+        o = torch.empty((n, heads * dim), dtype=torch.float16, device="cuda")
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(cache, heads, n, n, True), dtype=torch.uint8, device="cuda")
+        old = to_np(cache.weight[used]).astype(np.float64)
+        fq.flex_paged_attention(cache, torch.from_numpy(q).cuda().view(n, -1), heads * dim, heads, None, None, 0, o, None,
+                                None, n, ws, accumulate=True)
+        sync_status()
+        new = to_np(cache.weight[used]).astype(np.float64)
+        for h in (0, heads - 1):
+            for name, codes, meta in (("k", pools[0], pools[1]), ("v", pools[2], pools[3])):
+                ref.codes[name][:, 0], ref.meta[name][:, 0] = to_np(codes[used, h]), to_np(meta[used, h])
+            ro, _, sums, size = ref.attend(0, q[:, h:h + 1])
+            ep = 2 * (dim + 4) * E * size.max() + 2.0 ** -21
+            vmax = np.abs(ref.values("v", 0, 0)).max()
+            got = to_np(o).reshape(n, heads, dim)[:, h].astype(np.float64)
+            assert np.all(np.abs(got - ro[:, 0]) <= U * np.abs(ro[:, 0]) + (U + 2 * ep + held * (E + 2.0 ** -25)) * vmax)
+            was, now = (x[:, h].reshape(-1)[:held] for x in (old, new))
+            bound = (2 * ep + (held + n + 4) * E) * sums[0] + 2 * E * np.abs(was + sums[0]) + 1e-30
+            assert np.all(np.abs(now - was - sums[0]) <= bound), (n, h)
+    budget, recent = per * page // 3, 17
+    before = [to_np(x[used]) for x in (*pools, cache.weight, cache.slot_pos)]
+    new_len = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(cache, budget), dtype=torch.uint8, device="cuda")
+    fq.flex_paged_evict(cache, budget, recent, new_len, ew)
+    sync_status()
+    assert new_len.tolist() == [budget]
+    after = [to_np(x[used]) for x in (*pools, cache.weight, cache.slot_pos)]
+    for h in range(heads):
+        w, p = (x[:, h].reshape(-1)[:held] for x in before[4:])
+        first = p > p.max() - recent
+        order = np.lexsort((np.arange(held), -np.where(first, 0, w), ~first))
+        kept = np.zeros(held, bool)
+        kept[order[:budget]] = True
+        src = np.arange(per * page)
+        src[:budget][~kept[:budget]] = np.nonzero(kept)[0][kept[:budget].sum():]
+        for x, y in zip(before, after):
+            x, y = (t[:, h].reshape((per * page,) + t.shape[3:]) for t in (x, y))
+            assert np.array_equal(y.view(np.uint8), x[src].view(np.uint8)), h
+
+
+def test_replays_leave_the_same_cache_as_calls():
+    """A captured attention, store and eviction, replayed with other lengths and offsets: outputs,
+    slots, positions and weights have the bits that the same calls leave without a capture."""
+    c = Case(49, [700, 30, 0], heads=2, dim=64, room=64)
+    n0 = [1, 40, 9]
+    q, k, v = _scaled(c, n0, 4), [c.rows(m) for m in n0], [c.rows(m) for m in n0]
+    qd, cu, total, most = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    o = torch.empty((total, 4 * c.dim), dtype=torch.float16, device="cuda")
+    ls = torch.empty((total, 4), device="cuda")
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 4, total, most, True), dtype=torch.uint8, device="cuda")
+    ew = torch.empty(fq.flex_paged_evict_ws_bytes(c.cache, 25), dtype=torch.uint8, device="cuda")
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    state = [getattr(c.cache, x) for x in ("k_codes", "k_meta", "v_codes", "v_meta", "slot_pos", "weight")] + [o, ls, new]
+    start = [x.clone() for x in state]
+
+    def step():
+        fq.flex_paged_attention(c.cache, qd, qd.stride(0), 4, kd, vd, kd.stride(0), o, ls, cu, most, ws, accumulate=True,
+                                total=total)
+        fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), cu, most, total=total)
+        fq.flex_paged_evict(c.cache, 25, 5, new, ew)
+
+    def restore(n, ctx):
+        for x, y in zip(state, start):
+            x.copy_(y)
+        cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32))
+        c.set_ctx(ctx)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, ctx in ((n0, [700, 30, 0]), ([40, 1, 9], [650, 30, 0]), ([0, 0, 38], [700, 30, 26]), ([1, 1, 1], [0, 25, 26])):
+        restore(n, ctx)
+        step()
+        sync_status()
+        want = [x.clone() for x in state]
+        assert not torch.equal(want[5], start[5]) and want[8].tolist() == [min(x, 25) for x in ctx]
+        restore(n, ctx)
+        graph.replay()
+        sync_status()
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(state, want)), (n, ctx)
