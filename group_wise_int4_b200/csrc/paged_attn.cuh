@@ -12,11 +12,6 @@ __device__ __forceinline__ void cp16(uint32_t s, const void* g, bool ok) {
     const int n = ok ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_small(uint32_t s, const void* g, bool ok) {
-    const int n = ok ? N : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(s), "l"(g), "n"(N), "r"(n) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
