@@ -127,8 +127,8 @@ __device__ __forceinline__ uint32_t dequant_pair(uint32_t raw_pair_bits, uint32_
 }
 
 // Hardware reciprocal (rcp.approx, relative error below 2^-22); the result is rounded
-// to fp16 right after, so it matches the correctly rounded reciprocal except at rare
-// fp16 rounding ties.
+// to fp16 right after, which gives the correctly rounded fp16(1 / scale) for every fp16
+// scale (why, stands at step16_of in paged.cuh).
 __device__ __forceinline__ float rcp_approx(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -5,7 +5,9 @@
 //   lse_r = log sum_j exp(s_j),  o_r = sum_j exp(s_j - lse_r) v_j,
 // in one pass over the keys with a running maximum and sum; statistics are fp32. Probabilities
 // are fp16 operands of the value product: rounding them costs o about as much as its own
-// rounding does, which up to 4 rows is avoided (TWICE below).
+// rounding does (1.2 to 1.4 times the error against 64 bits, below one fp16 step of o), which
+// up to 4 rows is avoided (TWICE below); above, the second product would be half as many
+// again of all, for what the output's type mostly cannot show.
 // k_j and v_j are the fp16 values of paged.cuh, so the products are exact and summed in fp32.
 #include <type_traits>
 
@@ -26,13 +28,17 @@ namespace {
 // its scales into steps once, for all lanes that use them.
 //
 // Three instructions for two values (extract, subtract the exponent's offset, one fused
-// multiply-add) make about 220 of the 450 that 16 keys of 128 dims take at 4 bits, so the
-// issue slots bound it, not the memory: 144 sequences of 512 to 543 slots at 96 heads take
-// 307 us (3.5 TB/s, 53% of the measured copy bandwidth, 66% of the issue slots); 8-bit
-// codes of four sequences of 3001 to 60001 slots shared by 8 heads each 65 us (75%).
-// Warps of a multiprocessor, by registers: without spilling the kernel takes 168 at 8 rows of 128
-// dims (16 warps of 128 registers spill, and take 440 us instead of 338 for a decode step of
-// 144 sequences of 512 to 543 slots, 96 heads), 235 at 16.
+// multiply-add) make about 220 of the 450 that 16 keys of 128 dims take at 4 bits: 144
+// sequences of 512 to 543 slots at 96 heads take 307 us (3.5 TB/s, 53% of the measured copy
+// bandwidth) with 66% of the issue slots busy and 12 warps a multiprocessor, so latency is
+// part of it. It is no lower bound: the contiguous cache's kernel multiplies raw codes and
+// applies step and minimum to each group's sums, 370 instructions and 257 us for the same
+// sizes, with values rounded otherwise than here. 8-bit codes of four sequences of 3001 to
+// 60001 slots shared by 8 heads each: 65 us (75%).
+// Warps of a multiprocessor, by registers: at 128 dims the kernel takes 160 to 168 at 8 rows and
+// up to 235 at 16 without spilling (16 warps of 128 registers spill, and took 440 us instead
+// of 338 for the 144 sequences); at 64 dims 96 and 128 registers spill 20 to 92 bytes.
+// At 64 dims and 8 bits shared memory holds 16 of the 20 warps.
 constexpr int rows_warps(int dim, int rows) { return dim == 64 ? (rows == 8 ? 20 : 16) : (rows == 8 ? 12 : 8); }
 
 template <int D, int BITS, int GS, int NR>
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(RowsShape<D, BITS, GS, NR>::WARPS * 32, RowsSh
                 for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(sc[k][n][e] - m[n][e & 1], kLog2e, kLift));
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];
-                uint32_t h[2] = {half2_of(p[0], p[1]), half2_of(p[2], p[3])};
+                uint32_t h[2] = {half2_of(p[0], p[1]), half2_of(p[2], p[3])};     // (rounded: at the top of the file)
                 if (TWICE) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -541,10 +547,12 @@ __global__ void __launch_bounds__(128) paged_weight_one_kernel(AttnArgs A) {
 }
 
 // Any number of rows: the scores again (about 25 of the 71 us of 12 sequences with 1 to 97 new
-// tokens over up to 1500 slots, 32 heads of 64: latency of the first loads, then issue slots). A warp holds 32 keys as operands in registers and goes
-// through all query rows of the sequence, so every key's sum stays in its lanes and is added
-// in one fixed order; no atomics. Query rows pass through shared memory, 32 at a time, for 4
-// warps.
+// tokens over up to 1500 slots, 32 heads of 64: latency of the first loads, 49% of the issue slots;
+// 28 of 62 us of a decode step with 2 heads sharing 16 key heads). A warp holds 32 keys as
+// operands in registers and goes through all query rows of the sequence, so every key's sum
+// stays in its lanes and is added in one fixed order; no atomics. Query rows pass through
+// shared memory, 32 at a time, for 4 warps. The registers that fit 7 (64 dims) and 4 blocks
+// spill 4 to 24 bytes.
 template <int D, int BITS, int GS, bool LOOP>
 __global__ void __launch_bounds__(128, D == 64 ? 7 : 4) paged_weight_kernel(AttnArgs A) {
     const PagedView& c = A.c;

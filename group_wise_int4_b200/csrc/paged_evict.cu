@@ -12,15 +12,18 @@
 // consecutive slots a thread (one page lookup, two wide loads each of weights and positions),
 // finds the budget-th largest key bit by bit with counts over the block, lists the moves
 // with two block scans and copies. Nothing passes through memory but what has to; latency
-// and the search's issue slots bound it: 32 sequences of 1000 to 1040 slots cut to 1024 at 32
-// heads 13 us, 4 prompts of 500 to 2048 cut to 512 at 56 heads 14 (the two launches below:
-// 26 and 33). Longer tables: select and move below.
+// and the search's barriers bound it: 32 sequences of 1000 to 1040 slots cut to 1024 at 32
+// heads 12 us, 4 prompts of 500 to 2048 cut to 512 at 56 heads 13 (the two launches below,
+// by a table of a few more pages: 20 and 23). Longer tables, whatever their sequences hold:
+// select and move below.
 //
 // select: one block per (sequence, head). The keys (an order-preserving integer of the
 // weight, the largest value for the recent slots) go to shared memory once, the
 // budget-th largest is found digit by digit from histograms (11 + 11 + 10 bits), and one
 // ordered pass lists what is given up and what moves. Weights and positions are read
-// once (8 bytes a slot); the block's few synchronised passes over shared memory bound it.
+// once (8 bytes a slot); the block's few synchronised passes over shared memory bound it:
+// 8 sequences of 6000 slots cut to 4096 at 32 heads of 128 take 82 us (floor 17), 2 of
+// 40000 cut to 8192 at 8 heads 152 (16 blocks on the whole device).
 // move: 8 lanes copy one slot (codes, metadata, weight, position) to its place.
 #include "paged.cuh"
 

@@ -7,7 +7,7 @@
 //
 //   dequant warps   codes -> registers (a block of keys ahead) -> fp16 K and V in shared
 //                   memory; a thread takes a key or a value and works out its steps once
-//   matrix warps    S_t = Q_t K^T (both from shared memory), O_t += P_t V (P_t from tensor
+//   matrix warps    two a tile: S_t = Q_t K^T (both from shared memory), O_t += P_t V (P_t from tensor
 //                   memory, over S_t's columns; V as an MN-major operand, so K and V
 //                   have the same layout and neither is transposed)
 //   softmax warps   one row a thread: maximum, exp2, sum, P_t
@@ -19,11 +19,19 @@
 // (wait, S, softmax, P V in turn): 5100 cycles per 128 keys and 256 rows. One warp that
 // issues all products: 1745 us for 2000 tokens over 8 and 16 thousand slots at 32 heads of
 // 128, one a tile 1169, one for each kind and tile 1018, with the stages' release off its
-// path to the next scores 966 us, scores of any magnitude 986: 0.88 PFLOP/s, 53% of the
-// measured fp16 rate. What bounds
+// path to the next scores 966 us, scores of any magnitude 980 to 990 captured and replayed
+// (0.88 PFLOP/s, 53% of the measured fp16 rate) and 1000 to 1070 a call, by the device's
+// clock. What bounds
 // it now is the softmax warps: 2080 cycles a block of 64 keys, of which the exponential
 // unit is busy 1024. Tried and slower: the two tiles' exponentials in turns (1040), a
 // quarter of them as polynomials (1125), two threads a row.
+//
+// One tile: two blocks a multiprocessor leave 96 registers, and all forms spill 56 to 88 bytes (142
+// to 214 loaded); of two tiles only 8 bits with groups of 64 at 128 dims does (12).
+// Probabilities are rounded to fp16, as operands of the value product: o's error against 64
+// bits is 1.2 to 1.4 times that of fp32 probabilities, below one fp16 step; what the
+// rounding leaves would take a second product and as many conversions again in the softmax
+// warps, which bound the kernel.
 //
 // The running maximum m only moves when a score passes it by kSlack: until then the weights grow
 // instead of O being rescaled (fp16 holds them with the same relative error). The final
@@ -46,7 +54,7 @@ struct TileShape {
     static constexpr int QB = 128 * D * 2, BLOCK = NK * D * 2;     // bytes of a tile's queries, of a block of keys
     static constexpr int SMEM = TILES * QB + 2 * ST * BLOCK + 1024;
     static constexpr int COLS = TILES == 1 ? 256 : 512;            // tensor memory: TILES * (2 * NK + D) columns
-    static constexpr int SOFT = TILES * 4;                         // softmax warps, then 4 dequant warps and the matrix warp
+    static constexpr int SOFT = TILES * 4;                         // softmax warps, then 4 dequant warps, two matrix warps a tile
     static constexpr int THREADS = SOFT * 32 + 128 + 64 * TILES;
 };
 
