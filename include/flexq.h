@@ -401,8 +401,8 @@ int flex_paged_load_kv(const flex_paged_cache* cache, void* k_out, void* v_out, 
  *   a second time for it, in another order than for o: each p is then off by a factor of
  *   at most exp(2 (head_dim + 4) 2^-24 sum |q_i k_i|), and never above 1.
  * Infinities and NaN of a key or value reach the rows that attend to it, and no other row; an
- * infinite fresh value makes the sum infinite however small its weight (a stored one may give
- * NaN where its weight is below fp16's smallest).
+ * infinite fresh value makes the sum infinite however small its weight (a stored one makes it
+ * infinite or NaN).
  * A score of -infinity weighs nothing; a row that has no other gets zeros, as one without keys.
  * ws: flex_paged_attention_ws_bytes(...) bytes, nothing in it has to be set; calls that may
  * run at the same time need workspaces of their own. (With accumulate and one row a
