@@ -1170,3 +1170,34 @@ def test_replays_leave_the_same_cache_as_calls():
         graph.replay()
         sync_status()
         assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(state, want)), (n, ctx)
+
+
+@pytest.mark.parametrize("share", [1, 5, 100])
+def test_a_bound_far_above_the_rows(share):
+    """`most` is a bound only: 2^24 with a few rows in the sequences, in every call."""
+    most = 1 << 24
+    c = Case(50, [300, 0, 65], heads=2, dim=64, page=64, room=5)
+    n = [3, 5, 0]
+    q, k, v = _scaled(c, n, 2 * share), [c.rows(m) for m in n], [c.rows(m) for m in n]
+    qd, cu, total, _ = c.ragged(q)
+    kd, vd = c.ragged(k)[0], c.ragged(v)[0]
+    o = torch.full((total + TAIL, 2 * share * c.dim), 3.25, dtype=torch.float16, device="cuda")
+    ls = torch.empty((total, 2 * share), device="cuda")
+    ws = torch.empty(fq.flex_paged_attention_ws_bytes(c.cache, 2 * share, total, most, True), dtype=torch.uint8, device="cuda")
+    before = c.cache.weight.clone()
+    fq.flex_paged_attention(c.cache, qd, qd.stride(0), 2 * share, kd, vd, kd.stride(0), o, ls, cu, most, ws, accumulate=True, total=total)
+    sync_status()
+    c.check_attention(q, k, v, o[:total], ls, before)
+    assert bool((o[total:] == 3.25).all())
+    fq.flex_paged_store_kv(c.cache, kd, vd, kd.stride(0), cu, most, total=total)
+    for b in range(3):
+        c.ref.store(b, k[b], v[b])
+    c.set_ctx([303, 5, 65])
+    sync_status()
+    c.check_slots("added")
+    outs = [torch.full((total + TAIL, 2 * c.dim), 5.0, dtype=torch.float16, device="cuda") for _ in "kv"]
+    fq.flex_paged_load_kv(c.cache, *outs, 2 * c.dim, cu, most, total=total, start=torch.tensor([300, 0, 65], dtype=torch.int32, device="cuda"))
+    sync_status()
+    for x, i in zip(outs, (0, 1)):
+        ref = np.concatenate([c.ref.load(0, 300, 3)[i], c.ref.load(1, 0, 5)[i]]).reshape(total, -1)
+        assert np.array_equal(to_np(x[:total]).view(np.uint16), ref.view(np.uint16)) and bool((x[total:] == 5).all())
