@@ -29,15 +29,14 @@ int current_device() {
 }
 }  // namespace
 
-bool smem_attr_needed(const void* kernel, int bytes) {
+void set_smem(const void* kernel, int bytes) {
     static std::map<std::pair<const void*, int>, int> done;
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(g_mu);
     int& have = done[std::make_pair(kernel, dev)];
-    if (have >= bytes) return false;
-    have = bytes;
-    return true;
+    if (have >= bytes) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) have = bytes;
 }
 
 int sm_count() {

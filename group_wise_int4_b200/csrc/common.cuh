@@ -29,12 +29,12 @@ inline int launch_status() {
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device), so that it is
-// not called again while a stream is being captured into a graph.
-bool smem_attr_needed(const void* kernel, int bytes);
+// not called again while a stream is being captured into a graph. Another thread's call
+// for the same kernel returns once the limit is raised, not before.
+void set_smem(const void* kernel, int bytes);
 template <typename K>
 inline void set_smem_once(K kernel, int bytes) {
-    if (smem_attr_needed(reinterpret_cast<const void*>(kernel), bytes))
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    set_smem(reinterpret_cast<const void*>(kernel), bytes);
 }
 
 // Launch `kernel` on `st`, with programmatic stream serialisation when pdl is true.

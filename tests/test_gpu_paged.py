@@ -12,6 +12,10 @@ Tolerances, with u = 2^-11 (half a step of fp16) and e = 2^-24 (of fp32):
   The output: probabilities rounded to fp16 (u, and 2^-25 where they underflow, against a
   largest one of 1), sums of `keys` terms, and one rounding: u |o| + (u + 2 ep + keys e)
   max|v| + keys 2^-25 max|v|."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -22,6 +26,7 @@ from _helpers import sync_status, to_np
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U, E = 2.0 ** -11, 2.0 ** -24
 TAIL = 2
 
@@ -1201,3 +1206,41 @@ def test_a_bound_far_above_the_rows(share):
     for x, i in zip(outs, (0, 1)):
         ref = np.concatenate([c.ref.load(0, 300, 3)[i], c.ref.load(1, 0, 5)[i]]).reshape(total, -1)
         assert np.array_equal(to_np(x[:total]).view(np.uint16), ref.view(np.uint16)) and bool((x[total:] == 5).all())
+
+
+FIRST_CALLS = r"""
+import threading
+import torch
+import group_wise_int4_b200 as fq
+calls = []
+for most in (1, 40, 200):
+    for _ in range(8):
+        table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+        cache = fq.FlexPagedCache(table, torch.full((2,), 20, dtype=torch.int32, device="cuda"), 8, 64, 2, 64)
+        x = torch.zeros((2 * most, 3 * 128), dtype=torch.float16, device="cuda")
+        o = torch.empty((2 * most, 128), dtype=torch.float16, device="cuda")
+        ws = torch.empty(fq.flex_paged_attention_ws_bytes(cache, 2, 2 * most, most), dtype=torch.uint8, device="cuda")
+        calls.append((cache, x, o, ws, most, torch.cuda.Stream()))
+torch.cuda.synchronize()
+start, wrong = threading.Barrier(len(calls)), []
+def run(cache, x, o, ws, most, stream):
+    start.wait()
+    try:
+        fq.flex_paged_attention(cache, x, 384, 2, x[:, 128:], x[:, 256:], 384, o, None, None, most, ws, stream=stream)
+    except Exception as e:
+        wrong.append(repr(e))
+threads = [threading.Thread(target=run, args=c) for c in calls]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not wrong, wrong
+assert fq.flex_get_status() == fq.FLEX_OK
+print("fine")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """A kernel's first launch sets its shared memory; another thread's must not come between."""
+    for _ in range(3):
+        p = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=240)
+        assert p.returncode == 0 and "fine" in p.stdout, p.stdout + p.stderr
